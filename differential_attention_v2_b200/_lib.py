@@ -11,6 +11,7 @@ says how to build it.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -20,7 +21,8 @@ LIB_PATH = os.path.join(_PKG, "libdiffattn_v2.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE = 0, -1, -2, -3, -4
 
-_vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_vp, _i, _f, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+_ip = ctypes.POINTER(ctypes.c_int)
 
 _SIGNATURES = {
     "diffattn_v2_version": (_i, []),
@@ -51,6 +53,24 @@ _SIGNATURES = {
     "diffattn_v2_lambda_v2": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "diffattn_v2_prefill_fused_lambda": (_i, [_vp] * 8 + [_i] * 7 + [_vp]),
     "diffattn_v2_prefill_varlen_window": (_i, [_vp] * 6 + [_i] * 7 + [_vp]),
+    "diffattn_v2_prefill_window_sink": (_i, [_vp] * 5 + [_i] * 7 + [_vp]),
+    "diffattn_v2_prefill_varlen_window_sink": (_i, [_vp] * 6 + [_i] * 8 + [_vp]),
+    "diffattn_v2_prefill_window_sink_train": (_i, [_vp] * 7 + [_i] * 7 + [_vp]),
+    "diffattn_v2_prefill_varlen_window_sink_train": (_i, [_vp] * 8 + [_i] * 8 + [_vp]),
+    "diffattn_v2_backward_window_sink_workspace_size": (_sz, [_i] * 6),
+    "diffattn_v2_backward_window_sink": (_i, [_vp] * 11 + [_i] * 7 + [_vp, _sz, _vp]),
+    "diffattn_v2_backward_varlen_window_sink_workspace_size": (_sz, [_i] * 7),
+    "diffattn_v2_backward_varlen_window_sink": (_i, [_vp] * 12 + [_i] * 8 + [_vp, _sz, _vp]),
+    "diffattn_v2_decode_window_sink": (_i, [_vp] * 6 + [_i] * 7 + [_vp]),
+    "diffattn_v2_decode_paged_window_sink": (_i, [_vp] * 7 + [_i] * 9 + [_vp]),
+    "diffattn_v2_rope": (_i, [_vp] * 6 + [_ip] + [_i] * 5 + [_i64] * 4 + [_i] * 3 + [_vp]),
+    "diffattn_v2_rope_append_paged": (_i, [_vp] * 6 + [_ip, _i] + [_vp] * 5 + [_i] * 8 + [_i64] * 4 + [_i] * 2 + [_vp]),
+    "diffattn_v2_cache_extend": (_i, [_vp] * 5 + [_i] * 4 + [_vp]),
+    "diffattn_v2_cache_fork": (_i, [_vp] * 7 + [_i] * 5 + [_vp]),
+    "diffattn_v2_cache_trim": (_i, [_vp] * 4 + [_i] * 6 + [_vp]),
+    "diffattn_v2_cache_free": (_i, [_vp] * 5 + [_i] * 4 + [_vp]),
+    "diffattn_v2_cache_compact": (_i, [_vp] * 6 + [_i] * 3 + [_vp]),
+    "diffattn_v2_cache_copy_pages": (_i, [_vp] * 3 + [_i] * 2 + [_sz, _vp]),
     "diffattn_v2_device_error": (_i, [ctypes.POINTER(_i), _vp]),
     "diffattn_v2_decode_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
 }
@@ -110,8 +130,81 @@ def _need(t, name, dtype, ndim):
         raise ValueError(f"{name}: must be contiguous")
 
 
+def _expect(t, name, dtype, shape, device):
+    """A contiguous tensor of this dtype and shape on this device."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _shape(t, name, ndim):
+    """The device and sizes of a call's leading tensor."""
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return t.device, t.shape
+
+
+def _new(given, name, dtype, shape, device, stream):
+    """The caller's output tensor, or a new one that its stream may use."""
+    if given is not None:
+        _expect(given, name, dtype, shape, device)
+        return given
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                        else torch.cuda.ExternalStream(int(stream), device=device))
+    return t
+
+
+def _call(name, device, stream, *args):
+    """An entry point on the tensors' device and the given or that device's current stream."""
+    index = device.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device)
+    if index == torch._C._cuda_getDevice():
+        st = getattr(LIB, name)(*args, s)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(LIB, name)(*args, s)
+    if st != OK:
+        _check(st, name)
+
+
 def version() -> int:
     return LIB.diffattn_v2_version()
+
+
+def _attention_inputs(q, k, v, lam, device):
+    """Checks q [..., Hq, D], k and v [..., Hkv, D] and lam [..., Hq/2]; returns Hkv."""
+    *lead, Hq, D = q.shape
+    if k.dim() != q.dim():
+        raise ValueError(f"k: expected {q.dim()} dimensions, got shape {tuple(k.shape)}")
+    Hkv = k.shape[-2]
+    _expect(q, "q", torch.bfloat16, q.shape, device)
+    _expect(k, "k", torch.bfloat16, (*lead, Hkv, D), device)
+    _expect(v, "v", torch.bfloat16, (*lead, Hkv, D), device)
+    _expect(lam, "lam", torch.float32, (*lead, Hq // 2), device)
+    return Hkv
+
+
+def _sequences(cu_seqlens, device):
+    n = cu_seqlens.numel()
+    if n < 1:
+        raise ValueError("cu_seqlens: expected B + 1 entries")
+    _expect(cu_seqlens, "cu_seqlens", torch.int32, (n,), device)
+    return n - 1
+
+
+def _window_of_sink(window, causal):
+    if window is None or not causal:
+        raise ValueError("sink needs a causal window")
+    return int(window)
 
 
 def prefill(q, k, v, lam, out=None, causal=True, stream=None):
@@ -130,8 +223,16 @@ def prefill(q, k, v, lam, out=None, causal=True, stream=None):
     return out
 
 
-def prefill_window(q, k, v, lam, window, out=None, stream=None):
-    """bf16 causal prefill where query i sees only keys i-window+1 .. i."""
+def prefill_window(q, k, v, lam, window, out=None, stream=None, sink=None):
+    """bf16 causal prefill where query i sees only keys i-window+1 .. i, and with `sink` the
+    first `sink` keys too."""
+    if sink is not None:
+        device, (B, S, Hq, D) = _shape(q, "q", 4)
+        Hkv = _attention_inputs(q, k, v, lam, device)
+        out = _new(out, "out", torch.bfloat16, (B, S, Hq // 2, D), device, stream)
+        _call("diffattn_v2_prefill_window_sink", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              lam.data_ptr(), out.data_ptr(), B, S, Hq, Hkv, D, int(window), int(sink))
+        return out
     for t, n, nd in ((q, "q", 4), (k, "k", 4), (v, "v", 4)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 3)
@@ -165,9 +266,19 @@ def prefill_varlen(q, k, v, lam, cu_seqlens, max_seqlen, out=None, causal=True, 
     return out
 
 
-def prefill_varlen_window(q, k, v, lam, cu_seqlens, max_seqlen, window, out=None, stream=None):
+def prefill_varlen_window(q, k, v, lam, cu_seqlens, max_seqlen, window, out=None, stream=None, sink=None):
     """Causal sliding-window prefill of packed sequences (layouts of prefill_varlen): query i
-    of a sequence sees that sequence's keys i-window+1 .. i."""
+    of a sequence sees that sequence's keys i-window+1 .. i, and with `sink` its first `sink`
+    keys too."""
+    if sink is not None:
+        device, (T, Hq, D) = _shape(q, "q", 3)
+        Hkv = _attention_inputs(q, k, v, lam, device)
+        B = _sequences(cu_seqlens, device)
+        out = _new(out, "out", torch.bfloat16, (T, Hq // 2, D), device, stream)
+        _call("diffattn_v2_prefill_varlen_window_sink", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              lam.data_ptr(), out.data_ptr(), cu_seqlens.data_ptr(), B, int(max_seqlen), T, Hq, Hkv, D, int(window),
+              int(sink))
+        return out
     for t, n, nd in ((q, "q", 3), (k, "k", 3), (v, "v", 3)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 2)
@@ -199,10 +310,21 @@ def prefill_f32(q, k, v, lam, out=None, causal=True, stream=None):
     return out
 
 
-def prefill_train(q, k, v, lam, out=None, o_branch=None, lse=None, causal=True, window=None, stream=None):
+def prefill_train(q, k, v, lam, out=None, o_branch=None, lse=None, causal=True, window=None, stream=None, sink=None):
     """Training forward: prefill plus the per-head normalised O_b (bf16 [B,S,Hq,D]) and the
     log2-domain row log-sum-exp (fp32 [B,S,Hq]) that backward reads. Returns (out, o_branch, lse).
-    With `window` the causal sliding-window prefill (query i sees keys i-window+1 .. i)."""
+    With `window` the causal sliding-window prefill (query i sees keys i-window+1 .. i); with
+    `sink` besides, the first `sink` keys stay visible and o_branch is fp32."""
+    if sink is not None:
+        window = _window_of_sink(window, causal)
+        device, (B, S, Hq, D) = _shape(q, "q", 4)
+        Hkv = _attention_inputs(q, k, v, lam, device)
+        out = _new(out, "out", torch.bfloat16, (B, S, Hq // 2, D), device, stream)
+        o_branch = _new(o_branch, "o_branch", torch.float32, (B, S, Hq, D), device, stream)
+        lse = _new(lse, "lse", torch.float32, (B, S, Hq), device, stream)
+        _call("diffattn_v2_prefill_window_sink_train", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              lam.data_ptr(), out.data_ptr(), o_branch.data_ptr(), lse.data_ptr(), B, S, Hq, Hkv, D, window, int(sink))
+        return out, o_branch, lse
     for t, n, nd in ((q, "q", 4), (k, "k", 4), (v, "v", 4)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 3)
@@ -232,10 +354,40 @@ def backward_workspace_size(B, S, Hq) -> int:
     return int(LIB.diffattn_v2_backward_workspace_size(B, S, Hq))
 
 
+def _gradient_tensors(q, k, v, lam, o_branch, lse, dout, dq, dk, dv, dlam, device, stream):
+    """The backward's inputs and its gradient tensors (the caller's or new ones), in C order."""
+    *lead, Hq, D = q.shape
+    _expect(o_branch, "o_branch", torch.float32, q.shape, device)
+    _expect(lse, "lse", torch.float32, (*lead, Hq), device)
+    _expect(dout, "dout", torch.bfloat16, (*lead, Hq // 2, D), device)
+    grads = [_new(g, "d" + n, t.dtype, t.shape, device, stream)
+             for g, n, t in ((dq, "q", q), (dk, "k", k), (dv, "v", v), (dlam, "lam", lam))]
+    return [q, k, v, lam, o_branch, lse, dout, *grads]
+
+
+def _workspace(given, need, device, stream):
+    if given is None:
+        return _new(None, "workspace", torch.uint8, (max(need, 16),), device, stream)
+    if given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    return given
+
+
 def backward(q, k, v, lam, o_branch, lse, dout, causal=True, dq=None, dk=None, dv=None, dlam=None,
-             workspace=None, window=None, stream=None):
+             workspace=None, window=None, stream=None, sink=None):
     """Gradients of the bf16 prefill: returns (dq, dk, dv, dlam) with the layouts of q, k, v, lam.
-    With `window` the gradients of the causal sliding-window prefill."""
+    With `window` the gradients of the causal sliding-window prefill, with `sink` besides those
+    of the window with sinks (o_branch fp32)."""
+    if sink is not None:
+        window, sink = _window_of_sink(window, causal), int(sink)
+        device, (B, S, Hq, D) = _shape(q, "q", 4)
+        Hkv = _attention_inputs(q, k, v, lam, device)
+        ptrs = _gradient_tensors(q, k, v, lam, o_branch, lse, dout, dq, dk, dv, dlam, device, stream)
+        need = LIB.diffattn_v2_backward_window_sink_workspace_size(B, S, Hq, Hkv, window, sink)
+        workspace = _workspace(workspace, need, device, stream)
+        _call("diffattn_v2_backward_window_sink", device, stream, *(t.data_ptr() for t in ptrs), B, S, Hq, Hkv, D,
+              window, sink, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        return tuple(ptrs[7:])
     for t, n, nd in ((q, "q", 4), (k, "k", 4), (v, "v", 4), (o_branch, "o_branch", 4), (dout, "dout", 4)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 3)
@@ -268,10 +420,22 @@ def backward(q, k, v, lam, o_branch, lse, dout, causal=True, dq=None, dk=None, d
 
 
 def prefill_varlen_train(q, k, v, lam, cu_seqlens, max_seqlen, out=None, o_branch=None, lse=None, causal=True,
-                         stream=None, window=None):
+                         stream=None, window=None, sink=None):
     """Training forward of packed sequences (layouts of prefill_varlen): returns
     (out [T,Hq/2,D], o_branch [T,Hq,D], lse [T,Hq]). With `window` the causal sliding window
     inside every sequence."""
+    if sink is not None:  # with a window: the first `sink` keys stay visible, o_branch fp32
+        window = _window_of_sink(window, causal)
+        device, (T, Hq, D) = _shape(q, "q", 3)
+        Hkv = _attention_inputs(q, k, v, lam, device)
+        B = _sequences(cu_seqlens, device)
+        out = _new(out, "out", torch.bfloat16, (T, Hq // 2, D), device, stream)
+        o_branch = _new(o_branch, "o_branch", torch.float32, (T, Hq, D), device, stream)
+        lse = _new(lse, "lse", torch.float32, (T, Hq), device, stream)
+        _call("diffattn_v2_prefill_varlen_window_sink_train", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+              lam.data_ptr(), out.data_ptr(), o_branch.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), B,
+              int(max_seqlen), T, Hq, Hkv, D, window, int(sink))
+        return out, o_branch, lse
     for t, n, nd in ((q, "q", 3), (k, "k", 3), (v, "v", 3)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 2)
@@ -304,9 +468,21 @@ def backward_varlen_workspace_size(B, total_tokens, Hq) -> int:
 
 
 def backward_varlen(q, k, v, lam, o_branch, lse, dout, cu_seqlens, max_seqlen, causal=True, workspace=None,
-                    stream=None, window=None):
+                    stream=None, window=None, sink=None):
     """Gradients of the packed-sequence prefill: returns (dq, dk, dv, dlam) in the packed layouts.
     With `window` the gradients of the causal sliding-window packed prefill."""
+    if sink is not None:  # with a window: the first `sink` keys stay visible, o_branch fp32
+        window, sink = _window_of_sink(window, causal), int(sink)
+        device, (T, Hq, D) = _shape(q, "q", 3)
+        Hkv = _attention_inputs(q, k, v, lam, device)
+        B = _sequences(cu_seqlens, device)
+        ptrs = _gradient_tensors(q, k, v, lam, o_branch, lse, dout, None, None, None, None, device, stream)
+        need = LIB.diffattn_v2_backward_varlen_window_sink_workspace_size(B, int(max_seqlen), T, Hq, Hkv, window, sink)
+        workspace = _workspace(workspace, need, device, stream)
+        _call("diffattn_v2_backward_varlen_window_sink", device, stream, *(t.data_ptr() for t in ptrs),
+              cu_seqlens.data_ptr(), B, int(max_seqlen), T, Hq, Hkv, D, window, sink, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size())
+        return tuple(ptrs[7:])
     for t, n, nd in ((q, "q", 3), (k, "k", 3), (v, "v", 3), (o_branch, "o_branch", 3), (dout, "dout", 3)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 2)
@@ -339,9 +515,32 @@ def decode_workspace_size(B, Smax, Hq, Hkv, D) -> int:
     return int(LIB.diffattn_v2_decode_workspace_size(B, Smax, Hq, Hkv, D))
 
 
-def decode(q, kcache, vcache, seqlens, lam, out=None, workspace=None, stream=None, window=None):
+def _decode_inputs(q, kcache, vcache, seqlens, lam, window, lead):
+    """Checks the tensors of a decode step over caches [*lead, Hkv, D] (None: any extent)."""
+    if window is None:
+        raise ValueError("sink needs a window")
+    device, (B, Hq, D) = _shape(q, "q", 3)
+    if kcache.dim() != 4:
+        raise ValueError(f"cache: expected 4 dimensions, got shape {tuple(kcache.shape)}")
+    n, rows, Hkv, _ = kcache.shape
+    _expect(q, "q", torch.bfloat16, (B, Hq, D), device)
+    _expect(kcache, "K cache", torch.bfloat16, (n if lead is None else lead, rows, Hkv, D), device)
+    _expect(vcache, "V cache", torch.bfloat16, (n, rows, Hkv, D), device)
+    _expect(seqlens, "seqlens", torch.int32, (B,), device)
+    _expect(lam, "lam", torch.float32, (B, Hq // 2), device)
+    return device, B, Hq, Hkv, D, n, rows
+
+
+def decode(q, kcache, vcache, seqlens, lam, out=None, workspace=None, stream=None, window=None, sink=None):
     """bf16 decode step: q [B,Hq,D], caches [B,Smax,Hkv,D], seqlens int32 [B], lam fp32 [B,Hq/2].
-    With `window` the new token sees only its sequence's last `window` keys."""
+    With `window` the new token sees only its sequence's last `window` keys, with `sink` besides
+    the first `sink` ones (no workspace)."""
+    if sink is not None:
+        device, B, Hq, Hkv, D, _, Smax = _decode_inputs(q, kcache, vcache, seqlens, lam, window, q.shape[0])
+        out = _new(out, "out", torch.bfloat16, (B, Hq // 2, D), device, stream)
+        _call("diffattn_v2_decode_window_sink", device, stream, q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
+              seqlens.data_ptr(), lam.data_ptr(), out.data_ptr(), B, Smax, Hq, Hkv, D, int(window), int(sink))
+        return out
     _need(q, "q", torch.bfloat16, 3)
     _need(kcache, "kcache", torch.bfloat16, 4)
     _need(vcache, "vcache", torch.bfloat16, 4)
@@ -391,10 +590,20 @@ def decode_multi(q, kcache, vcache, seqlens, lam, out=None, workspace=None, stre
     return out
 
 
-def decode_paged(q, kpages, vpages, block_table, seqlens, lam, out=None, workspace=None, stream=None, window=None):
+def decode_paged(q, kpages, vpages, block_table, seqlens, lam, out=None, workspace=None, stream=None, window=None,
+                 sink=None):
     """bf16 decode over a paged cache: kpages/vpages [num_pages, page_size, Hkv, D],
     block_table int32 [B, max_pages], seqlens int32 [B], lam fp32 [B, Hq/2]. With `window`
-    the new token sees only its sequence's last `window` keys."""
+    the new token sees only its sequence's last `window` keys, with `sink` besides the first
+    `sink` ones (no workspace; entries of pages without a visible key may be -1)."""
+    if sink is not None:
+        device, B, Hq, Hkv, D, num_pages, page_size = _decode_inputs(q, kpages, vpages, seqlens, lam, window, None)
+        _expect(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), device)
+        out = _new(out, "out", torch.bfloat16, (B, Hq // 2, D), device, stream)
+        _call("diffattn_v2_decode_paged_window_sink", device, stream, q.data_ptr(), kpages.data_ptr(),
+              vpages.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), lam.data_ptr(), out.data_ptr(), B,
+              block_table.shape[1], page_size, num_pages, Hq, Hkv, D, int(window), int(sink))
+        return out
     _need(q, "q", torch.bfloat16, 3)
     _need(kpages, "kpages", torch.bfloat16, 4)
     _need(vpages, "vpages", torch.bfloat16, 4)
@@ -528,3 +737,199 @@ def decode_noalloc(q, kcache, vcache, seqlens, lam, out=None, stream=None):
                                         B, Smax, Hq, Hkv, D, _stream(stream, q.device))
     _check(st, "diffattn_v2_decode_noalloc")
     return out
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    return (ctypes.c_int * len(sections))(*sections), len(sections), sum(sections)
+
+
+def _heads(t, name, dtype, T, D, device):
+    """[T, H, D] with the heads of a token contiguous; returns H and the token stride."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name}: expected shape [{T}, heads, {D}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
+    H = t.shape[1]
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1) or (st < H * D and T > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return H, st if T > 1 else H * D
+
+
+def _rope_inputs(q, positions, inv_freq, sections):
+    device, (T, _, D) = _shape(q, "q", 3)
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"q: expected bfloat16 or float32, got {q.dtype}")
+    array, n_axes, pairs = _sections(tuple(sections))
+    _expect(positions, "positions", torch.int32, (n_axes, T), device)
+    _expect(inv_freq, "inv_freq", torch.float32, (pairs,), device)
+    Hq, q_stride = _heads(q, "q", q.dtype, T, D, device)
+    return device, T, D, Hq, q_stride, array, n_axes
+
+
+def rope(q, k, positions, inv_freq, sections, q_out=None, k_out=None, inverse=False, interleaved=False, stream=None):
+    """Rotary positions with len(sections) axes (1 to 4): q [T,Hq,D], k [T,Hkv,D] or None, bf16 or
+    fp32 (heads of a token contiguous, any token stride), positions int32 [n_axes, T], inv_freq
+    fp32 [sum(sections)]; pair c turns by positions[axis(c)] * inv_freq[c]. Pairs are dimensions
+    (c, c + P), interleaved (2c, 2c + 1); `inverse` turns back (the gradient). Outputs may be the
+    inputs. Returns (q_out, k_out)."""
+    device, T, D, Hq, q_stride, array, n_axes = _rope_inputs(q, positions, inv_freq, sections)
+    dtype = q.dtype
+    if q_out is None:
+        q_out, qo_stride = _new(None, "q_out", dtype, (T, Hq, D), device, stream), Hq * D
+    else:
+        h, qo_stride = _heads(q_out, "q_out", dtype, T, D, device)
+        if h != Hq:
+            raise ValueError(f"q_out: expected {Hq} heads, got {h}")
+    Hkv = k_stride = ko_stride = 0
+    if k is not None:
+        Hkv, k_stride = _heads(k, "k", dtype, T, D, device)
+        if k_out is None:
+            k_out, ko_stride = _new(None, "k_out", dtype, (T, Hkv, D), device, stream), Hkv * D
+        else:
+            h, ko_stride = _heads(k_out, "k_out", dtype, T, D, device)
+            if h != Hkv:
+                raise ValueError(f"k_out: expected {Hkv} heads, got {h}")
+    _call("diffattn_v2_rope", device, stream, q.data_ptr(), _ptr(k), q_out.data_ptr(),
+          None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), array, n_axes, T, Hq, Hkv,
+          D, q_stride, k_stride, qo_stride, ko_stride, _DTYPES[dtype], 1 if interleaved else 0, 1 if inverse else 0)
+    return q_out, None if k is None else k_out
+
+
+def rope_append_paged(q, k, v, positions, inv_freq, sections, kpages, vpages, block_table, seqlens, cu_seqlens=None,
+                      q_out=None, interleaved=False, stream=None):
+    """Rotary positions of a serving step's new tokens, with k (turned) and v written to their rows
+    of the paged cache: token i of sequence b's n_b new ones is logical position
+    seqlens[b] - n_b + i. q [T,Hq,D], k and v [T,Hkv,D] as in rope, caches
+    [num_pages, page_size, Hkv, D] of the same dtype; cu_seqlens int32 [B+1] tells the sequences'
+    new tokens (None: one each). Rows of q_out behind the last sequence are not written. Returns
+    q_out."""
+    device, T, D, Hq, q_stride, array, n_axes = _rope_inputs(q, positions, inv_freq, sections)
+    dtype = q.dtype
+    Hkv, k_stride = _heads(k, "k", dtype, T, D, device)
+    hv, v_stride = _heads(v, "v", dtype, T, D, device)
+    if kpages.dim() != 4 or hv != Hkv:
+        raise ValueError(f"caches [num_pages, page_size, {Hkv}, {D}] and v of {Hkv} heads are needed")
+    num_pages, page_size = kpages.shape[:2]
+    _expect(kpages, "kpages", dtype, (num_pages, page_size, Hkv, D), device)
+    _expect(vpages, "vpages", dtype, (num_pages, page_size, Hkv, D), device)
+    B = seqlens.numel() if cu_seqlens is None else _sequences(cu_seqlens, device)
+    _expect(seqlens, "seqlens", torch.int32, (B,), device)
+    _expect(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), device)
+    if q_out is None:
+        q_out, qo_stride = _new(None, "q_out", dtype, (T, Hq, D), device, stream), Hq * D
+    else:
+        h, qo_stride = _heads(q_out, "q_out", dtype, T, D, device)
+        if h != Hq:
+            raise ValueError(f"q_out: expected {Hq} heads, got {h}")
+    _call("diffattn_v2_rope_append_paged", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+          positions.data_ptr(), inv_freq.data_ptr(), array, n_axes, kpages.data_ptr(), vpages.data_ptr(),
+          block_table.data_ptr(), seqlens.data_ptr(), _ptr(cu_seqlens), T, B, block_table.shape[1], page_size,
+          num_pages, Hq, Hkv, D, q_stride, k_stride, v_stride, qo_stride, _DTYPES[dtype], 1 if interleaved else 0)
+    return q_out
+
+
+def _pool(block_table, refs, seqlens=None):
+    """Checks the state of a paged cache: block_table [B, max_pages], refs [num_pages], seqlens [B]."""
+    device, (B, max_pages) = _shape(block_table, "block_table", 2)
+    num_pages = refs.numel()
+    _expect(block_table, "block_table", torch.int32, (B, max_pages), device)
+    _expect(refs, "refs", torch.int32, (num_pages,), device)
+    if seqlens is not None:
+        _expect(seqlens, "seqlens", torch.int32, (B,), device)
+    return device, B, max_pages, num_pages
+
+
+def _result(given, device, stream, empty):
+    r = _new(given, "result", torch.int32, (1,), device, stream)
+    if empty:  # nothing is launched
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else torch.cuda.device(device):
+            r.zero_()
+    return r
+
+
+def cache_extend(block_table, seqlens, refs, n_new, page_size, result=None, stream=None):
+    """n_new[b] more tokens for every sequence: seqlens grows and the pages that are missing are
+    taken from the free ones (refs == 0), lowest first. Returns result int32 [1] on the device:
+    pages taken, or -1 (too few free pages or a full row; nothing changed)."""
+    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
+    _expect(n_new, "n_new", torch.int32, (B,), device)
+    result = _result(result, device, stream, B == 0)
+    _call("diffattn_v2_cache_extend", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
+          n_new.data_ptr(), result.data_ptr(), B, max_pages, int(page_size), num_pages)
+    return result
+
+
+def cache_fork(block_table, seqlens, refs, parents, children, page_size, copies=None, result=None, stream=None):
+    """Row children[i] (empty) continues what row parents[i] holds: whole pages are shared, a partly
+    filled last page gets a page of its own. Returns (copies int32 [n,2] for cache_copy_pages, -1
+    where there is none; result int32 [1]: pages taken, -1 too few free pages, -2 a bad pair)."""
+    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
+    n = parents.numel()
+    _expect(parents, "parents", torch.int32, (n,), device)
+    _expect(children, "children", torch.int32, (n,), device)
+    copies = _new(copies, "copies", torch.int32, (n, 2), device, stream)
+    if B == 0 and n > 0:
+        raise ValueError("parents: the table has no rows")
+    result = _result(result, device, stream, n == 0)
+    _call("diffattn_v2_cache_fork", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
+          parents.data_ptr(), children.data_ptr(), copies.data_ptr(), result.data_ptr(), n, B, max_pages,
+          int(page_size), num_pages)
+    return copies, result
+
+
+def cache_trim(block_table, seqlens, refs, page_size, window, sink, result=None, stream=None):
+    """Pages that hold neither one of the first `sink` keys nor one of the last `window` leave their
+    sequence. Returns result int32 [1]: pages that became free."""
+    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
+    result = _result(result, device, stream, B == 0)
+    _call("diffattn_v2_cache_trim", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
+          result.data_ptr(), B, max_pages, int(page_size), num_pages, int(window), int(sink))
+    return result
+
+
+def cache_free(block_table, seqlens, refs, seqs, result=None, stream=None):
+    """The listed sequences (int32; negative entries are padding) give their pages back and become
+    empty. Returns result int32 [1]: pages that became free, or -2 (an index >= B; nothing changed)."""
+    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
+    n = seqs.numel()
+    _expect(seqs, "seqs", torch.int32, (n,), device)
+    result = _result(result, device, stream, n == 0 or B == 0)
+    _call("diffattn_v2_cache_free", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
+          seqs.data_ptr(), result.data_ptr(), n, B, max_pages, num_pages)
+    return result
+
+
+def cache_compact(block_table, refs, block_table_out=None, refs_out=None, moves=None, result=None, stream=None):
+    """A plan that brings the L pages in use to the front of the pool. Returns (block_table, refs,
+    moves int32 [num_pages // 2, 2] for cache_copy_pages, result int32 [1] = L); the outputs may be
+    the inputs' own tensors."""
+    device, B, max_pages, num_pages = _pool(block_table, refs)
+    block_table_out = _new(block_table_out, "block_table_out", torch.int32, block_table.shape, device, stream)
+    refs_out = _new(refs_out, "refs_out", torch.int32, (num_pages,), device, stream)
+    moves = _new(moves, "moves", torch.int32, (num_pages // 2, 2), device, stream)
+    result = _new(result, "result", torch.int32, (1,), device, stream)
+    _call("diffattn_v2_cache_compact", device, stream, block_table.data_ptr(), refs.data_ptr(),
+          block_table_out.data_ptr(), refs_out.data_ptr(), moves.data_ptr(), result.data_ptr(), B, max_pages, num_pages)
+    return block_table_out, refs_out, moves, result
+
+
+def cache_copy_pages(kpages, vpages, copies, stream=None):
+    """Copies page copies[i][0] to page copies[i][1] in both caches [num_pages, ...]; pairs with a
+    negative entry are skipped. No page may be a destination twice, or a source and a destination."""
+    device = kpages.device
+    if not kpages.is_cuda or kpages.dim() < 2:
+        raise ValueError("kpages: must be a CUDA tensor [num_pages, ...]")
+    _expect(kpages, "kpages", kpages.dtype, kpages.shape, device)
+    _expect(vpages, "vpages", kpages.dtype, kpages.shape, device)
+    n = copies.shape[0]
+    _expect(copies, "copies", torch.int32, (n, 2), device)
+    num_pages = kpages.shape[0]
+    _call("diffattn_v2_cache_copy_pages", device, stream, kpages.data_ptr(), vpages.data_ptr(), copies.data_ptr(), n,
+          num_pages, kpages.numel() // max(num_pages, 1) * kpages.element_size())

@@ -93,6 +93,7 @@ struct Params {
   int* err;
   int B, S, S_pad, Hq, Hkv, causal;
   int window;                // causal sliding window: query i sees keys i-window+1 .. i (0: none)
+  int sink;                  // with a window: keys 0 .. sink-1 stay visible (kSink instances)
   int n_tiles;               // 128-row tiles
   const int* cu_seqlens;     // packed sequences: sequence b is rows cu[b] .. cu[b+1]-1 (null: [B,S])
   const int* pad_off;        // packed sequences: first row of sequence b in the row terms (128-aligned)
@@ -105,8 +106,20 @@ __host__ __device__ __forceinline__ size_t stat_index(size_t bp, int S_pad, int 
   return (bp * (S_pad / kStatBlock) + i / kStatBlock) * (kStatArrays * kStatBlock) + k * kStatBlock + i % kStatBlock;
 }
 
+// Four consecutive values of a head's O_b row, bf16 or (with sinks) fp32.
+__device__ __forceinline__ float4 load_o4(const __nv_bfloat16* o, int lane) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(o) + lane);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 load_o4(const float* o, int lane) {
+  return __ldg(reinterpret_cast<const float4*>(o) + lane);
+}
+
+template <typename TO>
 __global__ void __launch_bounds__(128)
-preprocess_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ o_branch,
+preprocess_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __restrict__ o_branch,
                   const float* __restrict__ lse, const float* __restrict__ lambda, float* __restrict__ stats,
                   float* __restrict__ dlam, int B, int S, int S_pad, int n_pairs) {
   const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -128,10 +141,8 @@ preprocess_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* _
   float e[2];
 #pragma unroll
   for (int br = 0; br < 2; ++br) {
-    const uint2 o = __ldg(reinterpret_cast<const uint2*>(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD) + lane);
-    const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
-    const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
-    float v = g0.x * o0.x + g0.y * o0.y + g1.x * o1.x + g1.y * o1.y;
+    const float4 o = load_o4(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD, lane);
+    float v = g0.x * o.x + g0.y * o.y + g1.x * o.z + g1.y * o.w;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     e[br] = v;
@@ -162,8 +173,9 @@ __global__ void pad_offsets_kernel(const int* __restrict__ cu, int* __restrict__
 // The preprocess for packed sequences: warp w is padded row pr of pair p (rows of all pairs
 // laid out as one batch of S_pad rows). Rows past a sequence's end, and past the padded
 // total, get -lse = -inf.
+template <typename TO>
 __global__ void __launch_bounds__(128)
-preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ o_branch,
+preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __restrict__ o_branch,
                          const float* __restrict__ lse, const float* __restrict__ lambda, float* __restrict__ stats,
                          float* __restrict__ dlam, const int* __restrict__ cu, const int* __restrict__ pad_off, int B,
                          int S_pad, int n_pairs) {
@@ -191,10 +203,8 @@ preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bflo
   float e[2];
 #pragma unroll
   for (int br = 0; br < 2; ++br) {
-    const uint2 o = __ldg(reinterpret_cast<const uint2*>(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD) + lane);
-    const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
-    const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
-    float v = g0.x * o0.x + g0.y * o0.y + g1.x * o1.x + g1.y * o1.y;
+    const float4 o = load_o4(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD, lane);
+    float v = g0.x * o.x + g0.y * o.y + g1.x * o.z + g1.y * o.w;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     e[br] = v;
@@ -360,7 +370,8 @@ __device__ __forceinline__ void tile_to_tmem(uint32_t tile, uint32_t trow, int r
 // --------------------------------------------------------------------------- dK / dV
 // kVarlen: packed sequences (p.cu_seqlens); kWindow: causal sliding window (p.window). The
 // plain [B,S] backward is the <false, false> instance and carries neither.
-template <bool kVarlen, bool kWindow>
+// kSink (with kWindow): keys 0 .. p.sink-1 stay visible to every later query.
+template <bool kVarlen, bool kWindow, bool kSink = false>
 __global__ void __launch_bounds__(kThreads, 1)
 dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
            const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -395,7 +406,8 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   const int nq = (S + 63) / 64;                     // 64-row query blocks
   const int q_first = p.causal ? k0 / 64 : 0;
   // with a window the tile's keys k0 .. k0+127 are seen by queries up to k0+127+window-1
-  const int q_end = kWindow ? min(nq, (k0 + 126 + p.window) / 64 + 1) : nq;
+  // (a tile with sinks by every later query)
+  const int q_end = kWindow && !(kSink && k0 < p.sink) ? min(nq, (k0 + 126 + p.window) / 64 + 1) : nq;
   const int steps_per_pair = q_end - q_first;
   const int n_steps = gpairs * steps_per_pair;
 
@@ -564,7 +576,7 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (key > qbase + c) p10 = p20 = 0.f;
             if (key > qbase + c + 1) p11 = p21 = 0.f;
           }
-          if (kWindow && wedge) {
+          if (kWindow && wedge && !(kSink && key < p.sink)) {
             if (qbase + c - key >= p.window) p10 = p20 = 0.f;
             if (qbase + c + 1 - key >= p.window) p11 = p21 = 0.f;
           }
@@ -576,10 +588,12 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           float u0, u1;
           f2_unpack(w, u0, u1);
           w_pk[c >> 1] = pack_bf16x2(u0, u1);
+          // query 0 sees one key: its softmax is constant (dP - E is rounding there, not zero)
+          const bool lone = kSink && c == 0 && qbase == 0;
           f2_unpack(d1, u0, u1);
-          d1_pk[c >> 1] = pack_bf16x2(u0, u1);
+          d1_pk[c >> 1] = pack_bf16x2(lone ? 0.f : u0, u1);
           f2_unpack(d2, u0, u1);
-          d2_pk[c >> 1] = pack_bf16x2(u0, u1);
+          d2_pk[c >> 1] = pack_bf16x2(lone ? 0.f : u0, u1);
         }
       }
       st_packed(trow + kTmS1 + col0, w_pk);
@@ -605,7 +619,7 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 }
 
 // --------------------------------------------------------------------------------- dQ
-template <bool kVarlen, bool kWindow>
+template <bool kVarlen, bool kWindow, bool kSink = false>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
@@ -640,7 +654,10 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
   // key blocks kb_first .. kb_first+n_steps-1 (64 keys each); with a window the rows
   // m0 .. m0+127 see keys from m0-window+1 on
   const int kb_first = kWindow ? max(0, m0 - p.window + 1) / 64 : 0;
-  const int n_steps = (p.causal ? min(nk, (m0 + 128) / 64) : nk) - kb_first;
+  // with sinks key blocks 0 .. n_head-1 come first
+  const int n_head = kSink ? min((p.sink + 63) / 64, kb_first) : 0;
+  const int n_steps = (p.causal ? min(nk, (m0 + 128) / 64) : nk) - kb_first + n_head;
+  auto key_block = [&](int t) -> int { return kSink && t < n_head ? t : kb_first + t - n_head; };
 
   const uint32_t tmem = setup(bar0, tmem_slot, abort_flag, warp);
 
@@ -661,9 +678,9 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
         const uint32_t st = sbase + kQOffX + s * kQStage;
         mbar_arrive_expect_tx(bar(kXFull + s), 2 * kStreamTile);
         for (int c = 0; c < 2; ++c) {
-          tma_load_4d(st + c * kStreamChunk, &tmK, bar(kXFull + s), c * 64, g, tok0 + 64 * (kb_first + t), tb);
+          tma_load_4d(st + c * kStreamChunk, &tmK, bar(kXFull + s), c * 64, g, tok0 + 64 * key_block(t), tb);
           tma_load_4d(st + kStreamTile + c * kStreamChunk, &tmV, bar(kXFull + s), c * 64, g,
-                      tok0 + 64 * (kb_first + t), tb);
+                      tok0 + 64 * key_block(t), tb);
         }
         issued = t + 1;
       }
@@ -752,8 +769,10 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
     // this row's terms (rows past S carry -lse = -inf: probabilities 0)
     const size_t bp = sb + pair;
     const int sr = srow0 + qi;  // this row in the row terms (past the sequence: -lse = -inf)
-    const float nl1 = __ldg(p.stats + stat_index(bp, p.S_pad, sr, 0));
-    const float nl2 = __ldg(p.stats + stat_index(bp, p.S_pad, sr, 1));
+    // (with sinks query 0 too: it sees one key, so its dS is 0 and dP - E is only rounding)
+    const bool lone = kSink && qi == 0;
+    const float nl1 = lone ? -INFINITY : __ldg(p.stats + stat_index(bp, p.S_pad, sr, 0));
+    const float nl2 = lone ? -INFINITY : __ldg(p.stats + stat_index(bp, p.S_pad, sr, 1));
     const uint64_t ne1 = f2_pack(__ldg(p.stats + stat_index(bp, p.S_pad, sr, 2)), __ldg(p.stats + stat_index(bp, p.S_pad, sr, 2)));
     const uint64_t ne2 = f2_pack(__ldg(p.stats + stat_index(bp, p.S_pad, sr, 3)), __ldg(p.stats + stat_index(bp, p.S_pad, sr, 3)));
     const float nlam_s = __ldg(p.stats + stat_index(bp, p.S_pad, sr, 4));
@@ -770,7 +789,7 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
       ld_cols_wait(s1);
       ld_cols_wait(s2);
       ld_cols_wait(dp);
-      const int kb = kb_first + t;  // key block (t drives the stages and barriers)
+      const int kb = key_block(t);  // t drives the stages and barriers
       const int kbase = 64 * kb + col0;
       // tile-uniform: keys past the query (causal diagonal) or past S (ragged last block);
       // keys before some row's window start (the window's lower edge)
@@ -792,8 +811,8 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
           if (kbase + c + 1 > lim) p11 = p21 = 0.f;
         }
         if (kWindow && wedge) {
-          if (kbase + c < lo) p10 = p20 = 0.f;
-          if (kbase + c + 1 < lo) p11 = p21 = 0.f;
+          if (kbase + c < lo && !(kSink && kbase + c < p.sink)) p10 = p20 = 0.f;
+          if (kbase + c + 1 < lo && !(kSink && kbase + c + 1 < p.sink)) p11 = p21 = 0.f;
         }
         const uint64_t dpp = f2_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
         const uint64_t d1 = f2_mul(f2_pack(p10, p11), f2_add(dpp, ne1));
@@ -848,7 +867,8 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
                                   const __nv_bfloat16* o_branch, const float* lse, const __nv_bfloat16* dout,
                                   __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float* dlambda,
                                   float* workspace, int* err, int B, int S, int Hq, int Hkv, int causal,
-                                  cudaStream_t stream, const int32_t* cu_seqlens, int total_tokens, int window) {
+                                  cudaStream_t stream, const int32_t* cu_seqlens, int total_tokens, int window,
+                                  int sink, const float* o_branch_f32) {
   using namespace bwd_tc;
   const int n_pairs = Hq / 2;
   Params p;
@@ -861,16 +881,25 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long warps = static_cast<long long>(S_pad) * n_pairs;
-    preprocess_varlen_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
-        dout, o_branch, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S_pad, n_pairs);
+    const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+    if (o_branch_f32)
+      preprocess_varlen_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch_f32, lse, lambda, workspace, dlambda,
+                                                           cu_seqlens, pad_off, B, S_pad, n_pairs);
+    else
+      preprocess_varlen_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch, lse, lambda, workspace, dlambda, cu_seqlens,
+                                                           pad_off, B, S_pad, n_pairs);
     p.S_pad = S_pad;
     p.pad_off = pad_off;
   } else {
     const int S_pad = (S + kRowPad - 1) / kRowPad * kRowPad;
     const long long warps = static_cast<long long>(B) * S_pad * n_pairs;
-    preprocess_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(dout, o_branch, lse, lambda,
-                                                                                    workspace, dlambda, B, S, S_pad,
-                                                                                    n_pairs);
+    const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+    if (o_branch_f32)
+      preprocess_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch_f32, lse, lambda, workspace, dlambda, B, S, S_pad,
+                                                    n_pairs);
+    else
+      preprocess_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch, lse, lambda, workspace, dlambda, B, S, S_pad,
+                                                    n_pairs);
     p.S_pad = S_pad;
     p.pad_off = nullptr;
   }
@@ -887,6 +916,7 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   p.Hkv = Hkv;
   p.causal = causal;
   p.window = window;
+  p.sink = window > 0 ? sink : 0;
   p.cu_seqlens = cu_seqlens;
   p.n_tiles = (S + 127) / 128;
   p.scale = 1.f / sqrtf(static_cast<float>(HD));
@@ -902,6 +932,12 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     kdq<<<dim3(B * n_pairs, p.n_tiles), kThreads, kQSmem, stream>>>(tmQ128, tmO128, tmK64, tmV64, p);
     return cudaGetLastError();
   };
+  if (o_branch_f32) {
+    // the sink form (window >= S: every earlier key, the causal mask)
+    if (window <= 0) p.window = S;
+    return cu_seqlens ? run(dkdv_sm100<true, true, true>, dq_sm100<true, true, true>)
+                      : run(dkdv_sm100<false, true, true>, dq_sm100<false, true, true>);
+  }
   if (cu_seqlens && window > 0) return run(dkdv_sm100<true, true>, dq_sm100<true, true>);
   if (cu_seqlens) return run(dkdv_sm100<true, false>, dq_sm100<true, false>);
   if (window > 0) return run(dkdv_sm100<false, true>, dq_sm100<false, true>);

@@ -9,16 +9,30 @@
 
 namespace da2 {
 
+// Host-side argument checks shared by the entry points of api_window_sink.cu and api_cache.cu.
+inline bool is_aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+// Hq even and the heads of every pair inside one KV group
+inline bool paired_heads(int Hq, int Hkv) { return Hq > 0 && Hkv > 0 && Hq % 2 == 0 && Hq % (2LL * Hkv) == 0; }
+// a page size that paged caches have: a power of two from 8 to 4096; its log2, or -1
+inline int page_shift_of(int page_size) {
+  if (page_size < 8 || page_size > 4096 || (page_size & (page_size - 1)) != 0) return -1;
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
 // bf16 prefill on tcgen05 (D = 128); window > 0 (causal only) limits query i to keys
 // i-window+1 .. i. With cu_seqlens (device, B+1 entries) the tensors hold B packed sequences
 // as one [1,T] batch and S is the longest sequence. Tensor maps: Q over [B,S,Hq,D], K/V over [B,S,Hkv,D],
 // boxes of 64 (d) x 1 (head) x 128 (rows) x 1, 128-byte swizzle; tmKh (optional) over K with
 // boxes of 64 (d) x 1 x 64 (rows) x 1, for the CTA-pair form (GQA groups of a multiple of 4);
-// tmO over out [B,S,Hq/2,D] (with cu_seqlens [1,T,Hq/2,D]) from encode_out_bf16.
+// tmO over out [B,S,Hq/2,D] (with cu_seqlens [1,T,Hq/2,D]) from encode_out_bf16. sink > 0 (with a
+// window): keys 0 .. sink-1 stay visible; the training forward then writes O_b in fp32.
 cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const CUtensorMap* tmKh, const CUtensorMap& tmO, const float* lambda, __nv_bfloat16* out, int* err, int B, int S,
                            int Hq, int Hkv, int causal, int window, const int* cu_seqlens, cudaStream_t stream,
-                           __nv_bfloat16* o_branch = nullptr, float* lse = nullptr);
+                           __nv_bfloat16* o_branch = nullptr, float* lse = nullptr, int sink = 0,
+                           float* o_branch_f32 = nullptr);
 
 // The [B,S] bf16 prefill with the V2 lambda computed in the kernel:
 // lambda[t, p] = sigmoid(x[t] . w_t[p] + bias[p]) with x [B*S, d_model] and w_t [Hq/2, d_model]
@@ -34,7 +48,8 @@ cudaError_t launch_prefill_lambda_fused(const CUtensorMap& tmQ, const CUtensorMa
 // dK/dV and dQ tile kernels. Tensor maps over q [B,S,Hq,D], dout [B,S,Hq/2,D], k and v
 // [B,S,Hkv,D] with 64- and 128-row boxes (64 d x 1 head). With cu_seqlens (device, B+1
 // entries) the tensors hold B packed sequences as one [1,T] batch (T = total_tokens) and S
-// is the longest sequence. window > 0 (causal only): query i saw keys i-window+1 .. i.
+// is the longest sequence. window > 0 (causal only): query i saw keys i-window+1 .. i. With
+// o_branch_f32 the sink form: keys 0 .. sink-1 too (o_branch unused).
 size_t backward_stats_bytes(int B, int S, int Hq);
 size_t backward_varlen_workspace_bytes(int B, int T, int Hq);
 cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& tmQ128, const CUtensorMap& tmO64,
@@ -44,7 +59,7 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
                                   __nv_bfloat16* dq, __nv_bfloat16* dk, __nv_bfloat16* dv, float* dlambda,
                                   float* workspace, int* err, int B, int S, int Hq, int Hkv, int causal,
                                   cudaStream_t stream, const int32_t* cu_seqlens = nullptr, int total_tokens = 0,
-                                  int window = 0);
+                                  int window = 0, int sink = 0, const float* o_branch_f32 = nullptr);
 
 // bf16 decode (D = 128): split kernel + combine. Tensor maps over the caches [B,Smax,Hkv,D],
 // boxes of 64 (d) x 1 x 64 (tokens) x 1, 128-byte swizzle. With block_table the maps cover
@@ -55,6 +70,36 @@ cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const 
                           float* ws_ml, int* counters, int* err, int B, int Smax, int Hq, int Hkv, int nsplit,
                           int split_len, const int32_t* block_table, int max_pages, int page_shift, int T,
                           cudaStream_t stream, int window = 0);
+
+// bf16 decode step (D = 128) over the last `window` and the first `sink` keys of each sequence:
+// one cluster per (KV head, sequence), no workspace. tmK, tmV as for launch_decode; tmK8, tmV8 the
+// same with boxes of 8 tokens.
+cudaError_t launch_decode_sink(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmK8,
+                               const CUtensorMap& tmV8, const __nv_bfloat16* q, const int32_t* seqlens,
+                               const float* lambda, __nv_bfloat16* out, int* err, int B, int Smax, int Hq, int Hkv,
+                               int window, int sink, const int32_t* block_table, int max_pages, int page_shift,
+                               cudaStream_t stream);
+
+// Page bookkeeping of a paged cache (cache_pages.cu): one cluster each; block tables
+// [B, max_pages], refs [num_pages]; result one int. At most kMaxCacheSeqs sequences (extend) or
+// pairs (fork).
+constexpr int kMaxCacheSeqs = 2048;
+cudaError_t launch_cache_extend(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_new,
+                                int32_t* result, int B, int max_pages, int page_shift, int num_pages,
+                                cudaStream_t stream);
+cudaError_t launch_cache_fork(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* parents,
+                              const int32_t* children, int32_t* copies, int32_t* result, int n, int B, int max_pages,
+                              int page_shift, int num_pages, cudaStream_t stream);
+cudaError_t launch_cache_trim(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B,
+                              int max_pages, int page_shift, int num_pages, int window, int sink,
+                              cudaStream_t stream);
+cudaError_t launch_cache_free(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result,
+                              int n, int B, int max_pages, int num_pages, cudaStream_t stream);
+cudaError_t launch_cache_compact(const int32_t* table, const int32_t* refs, int32_t* table_out, int32_t* refs_out,
+                                 int32_t* moves, int32_t* result, int B, int max_pages, int num_pages,
+                                 cudaStream_t stream);
+cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int n, int num_pages, size_t page_bytes,
+                                    cudaStream_t stream);
 
 // Tokens per split and number of splits of the bf16 decode for these sizes.
 void decode_split_plan(int B, int Smax, int Hkv, int* split_len, int* nsplit);
@@ -84,6 +129,23 @@ cudaError_t launch_decode_f32(const float* q, const float* kc, const float* vc, 
 // V1 lambda, broadcast to `rows` rows.
 cudaError_t launch_lambda_v1(const float* lq1, const float* lk1, const float* lq2, const float* lk2,
                              float lambda_init, int n_pairs, int d, int rows, float* out, cudaStream_t stream);
+
+// Rotary positions with n_axes axes (rope.cu): q [T,Hq,D] and k [T,Hkv,D] (token strides in
+// elements) to q_out and k_out. With block_table the k of every token goes to its row of the
+// paged cache k_out [num_pages, 1 << page_shift, Hkv, D], v to v_out; cu_seqlens null: token t is
+// sequence t's only new one.
+struct RopeParams {
+  const void *q, *k, *v;
+  void *q_out, *k_out, *v_out;
+  long long q_stride, k_stride, v_stride, qo_stride, ko_stride;
+  const int32_t* positions;  // [n_axes, T]
+  const float* inv_freq;     // [P]
+  int sec_end[4];            // first pair past each axis' section
+  int n_axes, P, T, Hq, Hkv, D, inverse, interleaved;
+  const int32_t *block_table, *seqlens, *cu_seqlens;
+  int B, max_pages, page_shift, num_pages;
+};
+cudaError_t launch_rope(const RopeParams& p, bool f32, cudaStream_t stream);
 
 // Address of the device error word on the current device.
 cudaError_t device_error_word(int** out);

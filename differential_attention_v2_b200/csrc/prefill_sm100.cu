@@ -130,10 +130,12 @@ struct Params {
   const float* lambda;    // [B,S,Hq/2]
   __nv_bfloat16* out;     // [B,S,Hq/2,D]
   __nv_bfloat16* o_branch;  // training forward: [B,S,Hq,D] per-head normalised O_b (null = inference)
+  float* o_branch_f32;      // training forward with sinks: the same in fp32
   float* lse;             // training forward: [B,S,Hq] log2-domain log-sum-exp of the scaled scores
   int* err;               // device error word
   int B, S, Hq, Hkv, causal;
   int window;             // causal sliding window (keys i-window+1 .. i); 0 = none
+  int sink;               // with a window: keys 0 .. sink-1 stay visible (kSink instances)
   const int* cu_seqlens;  // packed sequences: sequence b is tokens cu[b] .. cu[b+1]-1; null = [B,S]
   int n_row_tiles;
   int n_items;            // B * (Hq/2) * n_row_tiles
@@ -147,14 +149,22 @@ struct Params {
   int d_model;                  // a multiple of 8
 };
 
-// One work item: query rows m0 .. m0+127 of pair `pair` of sequence b, visiting KV tiles
-// j_first .. j_first+n_kv-1 (n_kv = 0: the tile lies past the end of a packed sequence).
+// One work item: query rows m0 .. m0+127 of pair `pair` of sequence b, visiting n_kv KV tiles:
+// with sinks tiles 0 .. n_sink-1, then tiles from j_first on (n_kv = 0: the query tile lies past
+// the end of a packed sequence).
 struct WorkItem {
   int b, pair, tile, m0;
   int S, tok0, tb;        // sequence length; its first row and batch index in the tensor maps
   int j_first, n_kv;
+  int n_sink;             // 0 without sinks
   size_t row_base;        // first output row of the sequence
 };
+
+// The it-th KV tile of an item.
+template <bool kSink>
+__device__ __forceinline__ int kv_tile(const WorkItem& w, int it) {
+  return kSink ? (it < w.n_sink ? it : w.j_first + it - w.n_sink) : w.j_first + it;
+}
 
 // Walk over the dense list of non-empty packed-sequence items: rank r holds row tile
 // t = n_row_tiles-1-r of the n_seq longest sequences (those with more than t row tiles, a
@@ -171,7 +181,7 @@ struct SortedCursor {
 // moves forward.
 // With kPair the unit of work is a pair of pairs of one KV head: cluster c takes the item and
 // its CTA of rank r computes pair 2u + r (u = the unit's index among the Hq/4 units).
-template <bool kVarlen, bool kWindow, bool kPair>
+template <bool kVarlen, bool kWindow, bool kPair, bool kSink>
 __device__ __forceinline__ bool work_item(const Params& p, int k, WorkItem& w, SortedCursor& cur,
                                           const int* seq_id, const int* seq_nt, int n_dense, uint32_t cta_rank) {
   constexpr int kCtas = kPair ? 2 : 1;
@@ -219,6 +229,7 @@ __device__ __forceinline__ bool work_item(const Params& p, int k, WorkItem& w, S
   if (w.m0 >= w.S) {
     w.j_first = 0;
     w.n_kv = 0;
+    w.n_sink = 0;
     return true;
   }
   const int n_kv_total = (w.S + BN - 1) / BN;
@@ -226,7 +237,9 @@ __device__ __forceinline__ bool work_item(const Params& p, int k, WorkItem& w, S
   // with a sliding window the first KV tile holds key m0 - window + 1 (or key 0)
   const int win_lo = w.m0 - p.window + 1;
   w.j_first = (kWindow && win_lo > 0) ? win_lo / BN : 0;
-  w.n_kv = j_last - w.j_first + 1;
+  // sink tiles before it: every row of the item sees their sink keys
+  w.n_sink = kSink ? min((p.sink + BN - 1) / BN, w.j_first) : 0;
+  w.n_kv = j_last - w.j_first + 1 + w.n_sink;
   return true;
 }
 
@@ -238,6 +251,16 @@ __device__ __forceinline__ void mask_row(uint32_t (&sr)[NC][32], int lo, int hi)
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (32 * c + e > hi || 32 * c + e < lo) sr[c][e] = __float_as_uint(-INFINITY);
+}
+
+// The same with sinks: columns below lo stay if they are below `sink`.
+template <int NC>
+__device__ __forceinline__ void mask_row_sink(uint32_t (&sr)[NC][32], int lo, int hi, int sink) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (32 * c + e > hi || (32 * c + e < lo && 32 * c + e >= sink)) sr[c][e] = __float_as_uint(-INFINITY);
 }
 
 // Max of this thread's NC x 32 raw scores: 3-input max, four independent chains.
@@ -420,7 +443,8 @@ __device__ __forceinline__ void arrive_for_mma(uint32_t bar, int lane) {
 //   * each softmax warp of either CTA arrives once on the even CTA's P and O-read barriers;
 //   * a wait that gives up raises the abort flag of both CTAs; both CTAs leave through one
 //     cluster barrier, after every copy and commit addressed to them has landed.
-template <bool kVarlen, bool kWindow, bool kPair, bool kLamFused = false>
+// kSink (with kWindow, one CTA per item): the first p.sink keys stay visible below the window.
+template <bool kVarlen, bool kWindow, bool kPair, bool kLamFused = false, bool kSink = false>
 __global__ void __launch_bounds__(kThreads, 1)
 diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKh,
@@ -525,7 +549,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         bool ok = true;
         // the even CTA announces the bytes of both CTAs' halves
         const uint32_t pair_mult = kPair ? 2u : 1u;
-        for (int k = 0; ok && work_item<kVarlen, kWindow, kPair>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank);
+        for (int k = 0; ok && work_item<kVarlen, kWindow, kPair, kSink>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank);
              ++k) {
           if (w.n_kv == 0) continue;
           // the single Q buffer is free once the previous item's last score GEMM has read it
@@ -544,7 +568,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           ++q_issued;
           const int g = (2 * w.pair) / group;
           for (int it = 0; it < w.n_kv; ++it) {
-            const int j = w.j_first + it;
+            const int j = kv_tile<kSink>(w, it);
             const int n = k_issued;  // this CTA's KV tile count so far
             const int s = n % kStages;
             const uint32_t ph = (n / kStages) & 1;
@@ -657,7 +681,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         int n_items = 0;  // items done
         // the four 128-column accumulators fill the 512 allocated columns from column 0
         bool ok = checked((tmem & 0xFFFFu) == 0u && kTmO2 + HD <= 512u, p.err);
-        for (int k = 0; ok && work_item<kVarlen, kWindow, kPair>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank);
+        for (int k = 0; ok && work_item<kVarlen, kWindow, kPair, kSink>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank);
              ++k) {
           if (w.n_kv == 0) continue;
           if (!(ok = pwait<kPair>(bar(kQFull), n_items & 1, abort_flag, flag_addr))) break;
@@ -714,7 +738,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const int n_pairs_l = p.Hq >> 1;
       int n_li = 0;  // items with KV tiles so far (the ring's count, as the softmax warps')
       bool ok = true;
-      for (int k = 0; ok && work_item<kVarlen, kWindow, kPair>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank);
+      for (int k = 0; ok && work_item<kVarlen, kWindow, kPair, kSink>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank);
            ++k) {
         if (w.n_kv == 0) continue;
         const int s = n_li & 1;
@@ -777,7 +801,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     int n_items = 0;  // items done
     bool ok = true;
 
-    for (int k = 0; ok && work_item<kVarlen, kWindow, kPair>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank); ++k) {
+    for (int k = 0; ok && work_item<kVarlen, kWindow, kPair, kSink>(p, k, w, cur, seq_id, seq_nt, n_dense, cta_rank); ++k) {
       if (w.n_kv == 0) continue;
       const int qi = w.m0 + r;  // query index of this row within its sequence
       const int S = w.S;
@@ -793,7 +817,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       float m_run = -INFINITY;
       float l_run = 0.f;
       for (int it = 0; it < w.n_kv; ++it) {
-        const int j = w.j_first + it;  // KV tile index (key position); n0 + it drives the barriers
+        const int j = kv_tile<kSink>(w, it);  // KV tile index (key position); n0 + it drives the barriers
         ok = __all_sync(0xffffffffu, pwait<kPair>(bar(kSFull + br), (n0 + it) & 1, abort_flag, flag_addr));
         if (!ok) break;
         tc_fence_after();
@@ -810,7 +834,8 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         // tile_masked is uniform over the CTA: every branch below that holds a warp-collective
         // tcgen05 instruction must be taken by all 32 lanes together
         // some row of the tile has keys of this KV tile below its window
-        const bool win_edge = kWindow && j * BN < w.m0 + BM - p.window;
+        // (with sinks: unless they cover the whole tile)
+        const bool win_edge = kWindow && j * BN < w.m0 + BM - p.window && !(kSink && (j + 1) * BN <= p.sink);
         const bool tile_masked = (p.causal && j == w.tile) || ((j + 1) * BN > S) || win_edge;
         // dead_h: no row of the warp sees a key of 64-key half h (the diagonal tile's upper
         // half for rows 0-63, a window's first tile's lower half for rows 64-127)
@@ -820,9 +845,16 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           if (p.causal && j == w.tile) hi = r;
           hi = min(hi, S - 1 - j * BN);
           const int lo = kWindow ? qi - p.window + 1 - j * BN : 0;
-          mask_row<4>(sr, lo, hi);
-          dead0 = __all_sync(0xffffffffu, hi < 0 || lo > 63);
-          dead1 = __all_sync(0xffffffffu, hi < 64 || lo > 127);
+          if constexpr (kSink) {
+            const int sk = p.sink - j * BN;  // columns below sk hold sinks
+            mask_row_sink<4>(sr, lo, hi, sk);
+            dead0 = __all_sync(0xffffffffu, hi < 0 || (lo > 63 && sk <= 0));
+            dead1 = __all_sync(0xffffffffu, hi < 64 || (lo > 127 && sk <= 64));
+          } else {
+            mask_row<4>(sr, lo, hi);
+            dead0 = __all_sync(0xffffffffu, hi < 0 || lo > 63);
+            dead1 = __all_sync(0xffffffffu, hi < 64 || lo > 127);
+          }
         }
         const float mx = row_max<4>(sr) * p.scale_log2;
 
@@ -944,6 +976,21 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
               store_row32(p.o_branch + ((w.row_base + qi) * p.Hq + 2 * w.pair + hb) * HD + col, ob);
             }
           }
+          if constexpr (kSink) {
+            if (p.o_branch_f32 != nullptr && row_valid) {
+#pragma unroll
+              for (int hb = 0; hb < 2; ++hb) {
+                const uint32_t* o = hb ? o2 : o1;
+                const float inv = hb ? inv2 : inv1;
+                float4* d = reinterpret_cast<float4*>(p.o_branch_f32 +
+                                                      ((w.row_base + qi) * p.Hq + 2 * w.pair + hb) * HD + col);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  d[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                     __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+              }
+            }
+          }
           uint32_t packed[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -1007,9 +1054,11 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                            const CUtensorMap* tmKh, const CUtensorMap& tmO, const float* lambda, __nv_bfloat16* out, int* err, int B, int S,
                            int Hq, int Hkv, int causal, int window, const int* cu_seqlens, cudaStream_t stream,
-                           __nv_bfloat16* o_branch, float* lse) {
+                           __nv_bfloat16* o_branch, float* lse, int sink, float* o_branch_f32) {
   using namespace prefill;
   Params p;
+  p.sink = window > 0 ? sink : 0;
+  p.o_branch_f32 = o_branch_f32;
   p.lambda = lambda;
   p.out = out;
   p.o_branch = o_branch;
@@ -1043,7 +1092,7 @@ cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   const char* env = getenv("DA2_PREFILL_CTA_PAIR");
   const bool pair_wanted = env != nullptr && env[0] == '1';
   const bool use_pair = pair_wanted && tmKh != nullptr && (group % 4) == 0 && !one_per_item &&
-                        !(cu_seqlens != nullptr && window > 0);
+                        !(cu_seqlens != nullptr && window > 0) && p.sink == 0 && o_branch_f32 == nullptr;
   if (use_pair) {
     p.n_items = B * (Hq / 4) * p.n_row_tiles;
     if (p.n_items == 0) return cudaSuccess;
@@ -1081,6 +1130,12 @@ cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
                                          : diffattn_prefill_sm100<true, false, false>)
                            : (window > 0 ? diffattn_prefill_sm100<false, true, false>
                                          : diffattn_prefill_sm100<false, false, false>);
+  // (a training forward that wants fp32 O_b takes the sink form whatever its window)
+  if (p.sink > 0 || o_branch_f32 != nullptr) {
+    kernel = cu_seqlens ? diffattn_prefill_sm100<true, true, false, false, true>
+                        : diffattn_prefill_sm100<false, true, false, false, true>;
+    if (window <= 0) p.window = S;  // every earlier key: the causal mask
+  }
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   if (p.n_items == 0) return cudaSuccess;

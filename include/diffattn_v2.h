@@ -80,6 +80,12 @@ enum {
   DA2_ERR_DEVICE = -4       /* a kernel recorded an internal error (bounded wait expired) */
 };
 
+/* Element types of the entry points that take more than one. */
+enum {
+  DA2_DTYPE_BF16 = 0,
+  DA2_DTYPE_F32 = 1
+};
+
 /* Library version: 100 * major + minor. */
 DA2_API int diffattn_v2_version(void);
 
@@ -446,6 +452,174 @@ DA2_API int diffattn_v2_prefill_fused_lambda(const void* q, const void* k, const
                                              const void* w_lambda_t, const float* bias, void* out,
                                              float* lambda_out, int B, int S, int Hq, int Hkv, int D, int d_model,
                                              int causal, da2_stream_t stream);
+
+/*
+ * Sliding-window attention with sinks: query i of a sequence sees its last `window` keys and the
+ * sequence's first `sink` keys,
+ *     key j visible from query i   iff   j <= i  and  (i - j < window  or  j < sink).
+ * The window is that of the "Attention variants" lesson, "Build it", Step 2, in the hybrid layers
+ * of the "Differential Attention (V2)" lesson's "Use it" section; the sinks are the few first
+ * tokens a trained window layer keeps leaning on after they have left its window. sink >= 0
+ * (sink = 0 is the window alone), window >= 1; a window or sinks of S keys or more are the plain
+ * causal mask. Layouts, arithmetic and errors as the window entry points of the same name, plus
+ * DA2_ERR_INVALID for sink < 0. Only KV tiles that hold a visible key are read.
+ *
+ * Masked keys weigh exactly 0, but 0 times a NaN or an infinity is a NaN: in the prefill and its
+ * backward a non-finite q, k, v or dout row reaches the rows of the 128-row tiles that load it
+ * (those of a packed neighbour too), as it does in the other prefill entry points.
+ */
+DA2_API int diffattn_v2_prefill_window_sink(const void* q, const void* k, const void* v, const float* lambda,
+                                            void* out, int B, int S, int Hq, int Hkv, int D, int window, int sink,
+                                            da2_stream_t stream);
+DA2_API int diffattn_v2_prefill_varlen_window_sink(const void* q, const void* k, const void* v, const float* lambda,
+                                                   void* out, const int32_t* cu_seqlens, int B, int max_seqlen,
+                                                   int total_tokens, int Hq, int Hkv, int D, int window, int sink,
+                                                   da2_stream_t stream);
+
+/*
+ * Training pass of the window with sinks. The forward's outputs and the backward's gradients are
+ * those of diffattn_v2_prefill_window_train / diffattn_v2_backward_window (and the packed forms),
+ * but o_branch is FP32 [B,S,Hq,D] ([T,Hq,D]): sinks draw most of a row's weight to one key, where
+ * dS = A (dO.v_j - dO.O_b) is a small difference of large terms that a bf16 O_b would drown. A
+ * query that sees a single key has a constant softmax: its dq, and its part of dk, are exactly 0.
+ * The workspace needs no initialisation; calls that share one must not overlap on the GPU. The
+ * result is deterministic (no atomics).
+ */
+DA2_API int diffattn_v2_prefill_window_sink_train(const void* q, const void* k, const void* v, const float* lambda,
+                                                  void* out, float* o_branch, float* lse, int B, int S, int Hq,
+                                                  int Hkv, int D, int window, int sink, da2_stream_t stream);
+DA2_API int diffattn_v2_prefill_varlen_window_sink_train(const void* q, const void* k, const void* v,
+                                                         const float* lambda, void* out, float* o_branch, float* lse,
+                                                         const int32_t* cu_seqlens, int B, int max_seqlen,
+                                                         int total_tokens, int Hq, int Hkv, int D, int window, int sink,
+                                                         da2_stream_t stream);
+DA2_API size_t diffattn_v2_backward_window_sink_workspace_size(int B, int S, int Hq, int Hkv, int window, int sink);
+DA2_API int diffattn_v2_backward_window_sink(const void* q, const void* k, const void* v, const float* lambda,
+                                             const float* o_branch, const float* lse, const void* dout, void* dq,
+                                             void* dk, void* dv, float* dlambda, int B, int S, int Hq, int Hkv, int D,
+                                             int window, int sink, void* workspace, size_t workspace_bytes,
+                                             da2_stream_t stream);
+DA2_API size_t diffattn_v2_backward_varlen_window_sink_workspace_size(int B, int max_seqlen, int total_tokens, int Hq,
+                                                                      int Hkv, int window, int sink);
+DA2_API int diffattn_v2_backward_varlen_window_sink(const void* q, const void* k, const void* v, const float* lambda,
+                                                    const float* o_branch, const float* lse, const void* dout,
+                                                    void* dq, void* dk, void* dv, float* dlambda,
+                                                    const int32_t* cu_seqlens, int B, int max_seqlen, int total_tokens,
+                                                    int Hq, int Hkv, int D, int window, int sink, void* workspace,
+                                                    size_t workspace_bytes, da2_stream_t stream);
+
+/*
+ * bf16 decode step of a window layer with sinks: the new token of sequence b (n = seqlens[b] keys,
+ * its own included) sees keys [max(0, n-window), n) and [0, min(sink, n)). Layouts as
+ * diffattn_v2_decode and diffattn_v2_decode_paged; no workspace, one launch; any number of calls
+ * may overlap. Every visible K/V row is read once. Rows that are not visible may hold anything,
+ * NaN included, and block-table entries of pages without a visible key are not read (they may be
+ * -1 or name a page of another sequence); the entry of a page with a visible key must be in
+ * [0, num_pages). An empty sequence gets zeros. Supported: D == 128, Hq/Hkv in {2, 4, 8, 16}.
+ */
+DA2_API int diffattn_v2_decode_window_sink(const void* q, const void* kcache, const void* vcache,
+                                           const int32_t* seqlens, const float* lambda, void* out, int B, int Smax,
+                                           int Hq, int Hkv, int D, int window, int sink, da2_stream_t stream);
+DA2_API int diffattn_v2_decode_paged_window_sink(const void* q, const void* kpages, const void* vpages,
+                                                 const int32_t* block_table, const int32_t* seqlens,
+                                                 const float* lambda, void* out, int B, int max_pages, int page_size,
+                                                 int num_pages, int Hq, int Hkv, int D, int window, int sink,
+                                                 da2_stream_t stream);
+
+/*
+ * Rotary positions with one to four axes on the heads of q and k (both heads of a pair and their
+ * keys turn alike). Pair c of token t turns by phi = positions[axis(c)][t] * inv_freq[c]:
+ *     (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi)
+ * sections[a] (a HOST array of n_axes ints) pairs belong to axis a, in order (time, height, width
+ * for images and video); P = their sum <= D/2. Pair c is dimensions (c, c + P), or (2c, 2c + 1)
+ * when interleaved = 1; dimensions from 2P on are copied. inverse = 1 turns by -phi: the gradient
+ * with respect to q and k given those of the outputs. Angles are formed in 64 bits, so positions
+ * may be any int32.
+ *   q, q_out [T,Hq,D]   k, k_out [T,Hkv,D] (Hkv = 0: no k)   of `dtype` (DA2_DTYPE_*), the token
+ *   stride of each in elements (>= H * D; heads of a token are contiguous), so that q and k may be
+ *   columns of one projection's output. An output may be its own input (same stride) and must
+ *   overlap nothing else.
+ *   positions int32 [n_axes, T]   inv_freq fp32 [P]
+ * D even; pointers aligned to their element (16-byte alignment of pointers, strides and sections is
+ * fastest). n_axes > 4 or D > 4096 give DA2_ERR_UNSUPPORTED.
+ */
+DA2_API int diffattn_v2_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                             const float* inv_freq, const int* sections, int n_axes, int T, int Hq, int Hkv, int D,
+                             int64_t q_stride, int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                             int dtype, int interleaved, int inverse, da2_stream_t stream);
+
+/*
+ * The same for the new tokens of a serving step, with their k (turned) and v written to a paged
+ * cache: token t of sequence b, the i-th of its n_b new ones, goes to logical position
+ * seqlens[b] - n_b + i (seqlens already counts them), i.e. row position % page_size of page
+ * block_table[b][position / page_size].
+ *   cu_seqlens int32 [B+1]: sequence b's new tokens are t = cu_seqlens[b] .. cu_seqlens[b+1]-1
+ *   (cu_seqlens[B] may be below T: the rows behind are not touched); NULL: one token per sequence
+ *   (T == B). A token whose position is negative or has no page (an entry outside
+ *   [0, num_pages)) gets its q and is not stored. Two tokens must not share a row.
+ * page_size is a power of two in [8, 4096].
+ */
+DA2_API int diffattn_v2_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
+                                          const int32_t* positions, const float* inv_freq, const int* sections,
+                                          int n_axes, void* kpages, void* vpages, const int32_t* block_table,
+                                          const int32_t* seqlens, const int32_t* cu_seqlens, int T, int B,
+                                          int max_pages, int page_size, int num_pages, int Hq, int Hkv, int D,
+                                          int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                                          int dtype, int interleaved, da2_stream_t stream);
+
+/*
+ * Pages of a paged cache. The caller owns the state; the calls change it on the device, one launch
+ * each, without host synchronisation, and must be ordered (one stream, or events):
+ *   block_table int32 [B, max_pages]  page of each logical page, -1 none
+ *   seqlens     int32 [B]             tokens of each sequence (0: an empty row)
+ *   refs        int32 [num_pages]     table entries that name the page; 0 = free
+ * One table serves every layer with the same window and sinks. Free pages are taken lowest index
+ * first, so the result of a call is unique. result int32 [1] (device) tells what happened; a call
+ * that refuses changes nothing else but `copies`, which it fills with -1.
+ *
+ * extend: n_new[b] (negative: 0) more tokens for every sequence: seqlens grows, and logical pages
+ *   that did not exist get a page, in the order of (b, logical page). result: pages taken, or -1:
+ *   the pool has too few free pages, or a sequence would need more than max_pages. B <= 2048.
+ * fork: row children[i] becomes a second owner of what row parents[i] holds: whole pages are
+ *   shared, a partly filled last page gets a page of its own, and copies[i] = (old page, new page)
+ *   lists the copy that diffattn_v2_cache_copy_pages has to make, once per layer; (-1, -1): none.
+ *   Pairs with a negative entry are padding. result: pages taken; -1: too few free pages; -2: an
+ *   index >= B, a child that is its parent, is not empty or is listed twice, or a parent longer
+ *   than its row. n <= 2048.
+ * trim: logical pages that hold neither one of the first `sink` keys nor one of the last `window`
+ *   leave their sequence (entry -1), as no later query of such a layer sees them. result: pages
+ *   that became free.
+ * free: the n listed sequences give all their pages back and become empty; negative entries are
+ *   padding, a sequence listed twice is freed once. result: pages that became free; -2: an index
+ *   >= B.
+ * compact: with L pages in use, the r-th used page at index >= L moves to the r-th free index
+ *   below L. Writes the new table and refs (which may be the old ones' buffers), moves int32
+ *   [num_pages/2, 2] = (from, to) by ascending index, then (-1, -1), for copy_pages (once per
+ *   layer), and result: L. Pages L .. num_pages-1 are then free.
+ */
+DA2_API int diffattn_v2_cache_extend(int32_t* block_table, int32_t* seqlens, int32_t* refs, const int32_t* n_new,
+                                     int32_t* result, int B, int max_pages, int page_size, int num_pages,
+                                     da2_stream_t stream);
+DA2_API int diffattn_v2_cache_fork(int32_t* block_table, int32_t* seqlens, int32_t* refs, const int32_t* parents,
+                                   const int32_t* children, int32_t* copies, int32_t* result, int n, int B,
+                                   int max_pages, int page_size, int num_pages, da2_stream_t stream);
+DA2_API int diffattn_v2_cache_trim(int32_t* block_table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B,
+                                   int max_pages, int page_size, int num_pages, int window, int sink,
+                                   da2_stream_t stream);
+DA2_API int diffattn_v2_cache_free(int32_t* block_table, int32_t* seqlens, int32_t* refs, const int32_t* seqs,
+                                   int32_t* result, int n, int B, int max_pages, int num_pages, da2_stream_t stream);
+DA2_API int diffattn_v2_cache_compact(const int32_t* block_table, const int32_t* refs, int32_t* block_table_out,
+                                      int32_t* refs_out, int32_t* moves, int32_t* result, int B, int max_pages,
+                                      int num_pages, da2_stream_t stream);
+
+/*
+ * Copies page copies[i][0] to page copies[i][1] in both caches, i < n; pairs with an entry outside
+ * [0, num_pages) are skipped. page_bytes = page_size * Hkv * D * element size, a multiple of 16
+ * (else DA2_ERR_UNSUPPORTED). No page may be listed as a destination twice, or as a source and a
+ * destination (fork and compact list none).
+ */
+DA2_API int diffattn_v2_cache_copy_pages(void* kpages, void* vpages, const int32_t* copies, int n, int num_pages,
+                                         size_t page_bytes, da2_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the device error word that kernels set when a

@@ -89,16 +89,17 @@ def causal_mask(n_q: int, n_k: int, q_offset: int = 0) -> np.ndarray:
     return _additive(j <= i)
 
 
-def window_mask(n_q: int, n_k: int, window: int, q_offset: int = 0) -> np.ndarray:
+def window_mask(n_q: int, n_k: int, window: int, q_offset: int = 0, sink: int = 0) -> np.ndarray:
     """Causal sliding window of [L07] ("Sliding window attention", its W = 4 figure and the
     key-terms table): query i sees its last `window` keys, i.e. key j with
     i - window < j <= i (the window holds the query's own key). window >= n gives the full
-    causal mask; window = 1 leaves only j = i."""
+    causal mask; window = 1 leaves only j = i. With `sink` the first `sink` keys stay visible
+    to every later query: j <= i and (i - window < j or j < sink)."""
     if window < 1:
         raise ValueError("window must be >= 1")
     i = np.arange(q_offset, q_offset + n_q)[:, None]
     j = np.arange(n_k)[None, :]
-    return _additive((j <= i) & (i - j < window))
+    return _additive((j <= i) & ((i - j < window) | (j < sink)))
 
 
 def pair_layout(Hq: int, Hkv: int):
@@ -145,14 +146,15 @@ def _f64(t) -> np.ndarray:
     return np.asarray(t, dtype=np.float64)
 
 
-def prefill(q, k, v, lam, causal: bool = True, row_block: int = 512, window=None) -> np.ndarray:
+def prefill(q, k, v, lam, causal: bool = True, row_block: int = 512, window=None, sink: int = 0) -> np.ndarray:
     """Forward prefill over the whole batch: out[B, S, Hq/2, D] in float64.
 
     q [B,S,Hq,D], k/v [B,S,Hkv,D], lam [B,S,Hq/2]. For every batch b and pair p the rows are
     processed in blocks of `row_block` (a memory bound only: every row is computed exactly
     as the definition states, over all its visible keys). `window` (causal only) restricts
     each query to its last `window` keys, the DiffAttn + sliding-window combination that the
-    lesson's "Use it" section names for hybrid layers, with the window of `window_mask`.
+    lesson's "Use it" section names for hybrid layers, with the window (and `sink`) of
+    `window_mask`.
     """
     if window is not None and not causal:
         raise ValueError("a sliding window is defined for causal attention")
@@ -167,7 +169,7 @@ def prefill(q, k, v, lam, causal: bool = True, row_block: int = 512, window=None
                 r1 = min(S, r0 + row_block)
                 n_k = r1 if causal else S
                 if window is not None:
-                    mask = window_mask(r1 - r0, n_k, window, r0)
+                    mask = window_mask(r1 - r0, n_k, window, r0, sink)
                 else:
                     mask = causal_mask(r1 - r0, n_k, r0) if causal else np.zeros((r1 - r0, S))
                 out[b, r0:r1, p] = diff_attention_block(
@@ -175,7 +177,7 @@ def prefill(q, k, v, lam, causal: bool = True, row_block: int = 512, window=None
     return out
 
 
-def prefill_varlen(q, k, v, lam, cu_seqlens, causal: bool = True, window=None) -> np.ndarray:
+def prefill_varlen(q, k, v, lam, cu_seqlens, causal: bool = True, window=None, sink: int = 0) -> np.ndarray:
     """Prefill of sequences packed along the token axis: q [T,Hq,D], k/v [T,Hkv,D],
     lam [T,Hq/2], sequence b = tokens cu_seqlens[b] .. cu_seqlens[b+1]-1. Every sequence is an
     independent prefill (its queries see only its own keys); with `window` (causal only) the
@@ -188,14 +190,14 @@ def prefill_varlen(q, k, v, lam, cu_seqlens, causal: bool = True, window=None) -
         s0, s1 = cu[b], cu[b + 1]
         if s1 > s0:
             out[s0:s1] = prefill(q[None, s0:s1], k[None, s0:s1], v[None, s0:s1], lam[None, s0:s1], causal=causal,
-                                 window=window)[0]
+                                 window=window, sink=sink)[0]
     return out
 
 
-def prefill_backward(q, k, v, lam, dout, causal: bool = True, window=None):
+def prefill_backward(q, k, v, lam, dout, causal: bool = True, window=None, sink: int = 0):
     """Gradients of the prefill: returns (dq [B,S,Hq,D], dk, dv [B,S,Hkv,D], dlam [B,S,Hq/2])
     for an upstream gradient dout [B,S,Hq/2,D], all float64. With `window` (causal only) the
-    mask is the sliding window of `window_mask`.
+    mask is the sliding window (with `sink` keys) of `window_mask`.
 
     The chain rule applied to the definition of `diff_attention_block`, per pair p (heads h1,
     h2 over KV head g) and batch b, with A_b = softmax(S_b), S_b = Q_b K^T / sqrt(D) + mask,
@@ -216,7 +218,7 @@ def prefill_backward(q, k, v, lam, dout, causal: bool = True, window=None):
     dv = np.zeros_like(v)
     dlam = np.zeros_like(lam)
     if window is not None:
-        mask = window_mask(S, S, int(window))
+        mask = window_mask(S, S, int(window), sink=sink)
     else:
         mask = causal_mask(S, S) if causal else np.zeros((S, S))
     for b in range(B):
@@ -237,7 +239,7 @@ def prefill_backward(q, k, v, lam, dout, causal: bool = True, window=None):
     return dq, dk, dv, dlam
 
 
-def prefill_backward_varlen(q, k, v, lam, dout, cu_seqlens, causal: bool = True, window=None):
+def prefill_backward_varlen(q, k, v, lam, dout, cu_seqlens, causal: bool = True, window=None, sink: int = 0):
     """Gradients of `prefill_varlen` for packed sequences (q [T,Hq,D], k/v [T,Hkv,D],
     lam [T,Hq/2], dout [T,Hq/2,D]): every sequence is an independent prefill, so its
     gradients are those of its own prefill and no token of one sequence has a gradient
@@ -250,7 +252,7 @@ def prefill_backward_varlen(q, k, v, lam, dout, cu_seqlens, causal: bool = True,
         s0, s1 = cu[b], cu[b + 1]
         if s1 > s0:
             g = prefill_backward(q[None, s0:s1], k[None, s0:s1], v[None, s0:s1], lam[None, s0:s1],
-                                 dout[None, s0:s1], causal=causal, window=window)
+                                 dout[None, s0:s1], causal=causal, window=window, sink=sink)
             dq[s0:s1], dk[s0:s1], dv[s0:s1], dlam[s0:s1] = (x[0] for x in g)
     return dq, dk, dv, dlam
 
@@ -311,13 +313,13 @@ def prefill_rows(q, k, v, lam, rows, causal: bool = True) -> np.ndarray:
     return np.stack(res) if res else np.zeros((0, q.shape[3]))
 
 
-def decode(q, kcache, vcache, seqlens, lam, window=None) -> np.ndarray:
+def decode(q, kcache, vcache, seqlens, lam, window=None, sink: int = 0) -> np.ndarray:
     """One decode step: out[B, Hq/2, D] in float64.
 
     q [B,Hq,D] is the new token's query; the caches [B,Smax,Hkv,D] already hold its key and
     value, and sequence b attends to keys [0, seqlens[b]), or with `window` to its last
     `window` keys [max(0, seqlens[b]-window), seqlens[b]) (the sliding window of the
-    "Attention variants" lesson for the newest query). lam [B,Hq/2]. A sequence with
+    "Attention variants" lesson for the newest query) and its first `sink` ones. lam [B,Hq/2]. A sequence with
     seqlens[b] == 0 has no visible key; its output is defined as 0.
     """
     B, Hq, D = q.shape
@@ -329,23 +331,24 @@ def decode(q, kcache, vcache, seqlens, lam, window=None) -> np.ndarray:
             continue
         n0 = max(0, n - int(window)) if window is not None else 0
         for g in range(Hkv):
-            kk = _f64(kcache[b, n0:n, g])
-            vv = _f64(vcache[b, n0:n, g])
+            keys = [j for j in range(n) if j >= n0 or j < sink]
+            kk = _f64(kcache[b, :n, g])[keys]
+            vv = _f64(vcache[b, :n, g])[keys]
             for p, h1, h2, gg in pair_layout(Hq, Hkv):
                 if gg != g:
                     continue
                 q1 = _f64(q[b, h1])[None, :]
                 q2 = _f64(q[b, h2])[None, :]
                 lm = np.array([float(lam[b, p])], dtype=np.float64)
-                out[b, p] = diff_attention_block(q1, q2, kk, vv, lm, np.zeros((1, n - n0)))[0]
+                out[b, p] = diff_attention_block(q1, q2, kk, vv, lm, np.zeros((1, len(keys))))[0]
     return out
 
 
-def decode_paged(q, kpages, vpages, block_table, seqlens, lam, window=None) -> np.ndarray:
+def decode_paged(q, kpages, vpages, block_table, seqlens, lam, window=None, sink: int = 0) -> np.ndarray:
     """Decode step over a paged cache: kpages/vpages [P, page_size, Hkv, D]; logical token t
     of sequence b lives in page block_table[b][t // page_size] at row t % page_size. The
-    sequence's logical cache is gathered page by page, then `decode` (with `window`) applies
-    as written."""
+    sequence's logical cache is gathered page by page, then `decode` (with `window` and
+    `sink`) applies as written."""
     page_size = int(kpages.shape[1])
     B = q.shape[0]
     outs = []
@@ -355,7 +358,7 @@ def decode_paged(q, kpages, vpages, block_table, seqlens, lam, window=None) -> n
         pages = [int(block_table[b][i]) for i in range(n_pages)]
         kc = np.concatenate([_f64(kpages[pg]) for pg in pages], axis=0)[:n] if n else np.zeros((0,) + tuple(kpages.shape[2:]))
         vc = np.concatenate([_f64(vpages[pg]) for pg in pages], axis=0)[:n] if n else np.zeros((0,) + tuple(vpages.shape[2:]))
-        outs.append(decode(q[b:b + 1], kc[None], vc[None], [n], lam[b:b + 1], window=window)[0])
+        outs.append(decode(q[b:b + 1], kc[None], vc[None], [n], lam[b:b + 1], window=window, sink=sink)[0])
     return np.stack(outs)
 
 
