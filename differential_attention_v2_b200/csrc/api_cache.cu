@@ -15,7 +15,7 @@ int rope_common(da2::RopeParams* p, const int32_t* positions, const float* inv_f
                 int T, int Hq, int Hkv, int D, int dtype, int interleaved, int inverse) {
   if (T < 0 || Hq <= 0 || Hkv < 0 || D <= 0 || D % 2 != 0 || n_axes < 1 || !sections) return DA2_ERR_INVALID;
   if ((dtype != DA2_DTYPE_BF16 && dtype != DA2_DTYPE_F32) || (interleaved & ~1) || (inverse & ~1)) return DA2_ERR_INVALID;
-  if (n_axes > 4 || D > 4096) return DA2_ERR_UNSUPPORTED;
+  if (n_axes > 4 || D > 4096 || Hq > 65536 || Hkv > 65536) return DA2_ERR_UNSUPPORTED;
   long long P = 0;
   for (int a = 0; a < n_axes; ++a) {
     if (sections[a] < 0) return DA2_ERR_INVALID;

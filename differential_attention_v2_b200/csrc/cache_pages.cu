@@ -429,21 +429,25 @@ constexpr int kPieceVecs = kCopyThreads * kCopyUnroll;
 __global__ void __launch_bounds__(kCopyThreads)
 copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const int2* __restrict__ copies, int n, int num_pages,
             int page_vecs, int pieces) {
-  for (long long it = blockIdx.x; it < static_cast<long long>(n) * 2 * pieces; it += gridDim.x) {
-    const long long u = it / pieces;
-    const int2 c = __ldg(copies + (u >> 1));
+  const long long items = static_cast<long long>(n) * 2 * pieces;
+  long long it = blockIdx.x;
+  if (it >= items) return;
+  int2 next = __ldg(copies + it / pieces / 2);
+  for (; it < items; it += gridDim.x) {
+    const int2 c = next;
+    if (it + gridDim.x < items) next = __ldg(copies + (it + gridDim.x) / pieces / 2);  // while this piece is copied
     if (c.x < 0 || c.y < 0 || c.x >= num_pages || c.y >= num_pages) continue;
-    uint4* pool = (u & 1) ? v : k;
+    uint4* pool = (it / pieces) & 1 ? v : k;
     const uint4* src = pool + static_cast<size_t>(c.x) * page_vecs;
     uint4* dst = pool + static_cast<size_t>(c.y) * page_vecs;
     const int at = static_cast<int>(it % pieces) * kPieceVecs + threadIdx.x;
     uint4 x[kCopyUnroll];
 #pragma unroll
     for (int i = 0; i < kCopyUnroll; ++i)
-      if (at + i * kCopyThreads < page_vecs) x[i] = src[at + i * kCopyThreads];
+      if (at + i * kCopyThreads < page_vecs) x[i] = __ldcs(src + at + i * kCopyThreads);
 #pragma unroll
     for (int i = 0; i < kCopyUnroll; ++i)
-      if (at + i * kCopyThreads < page_vecs) dst[at + i * kCopyThreads] = x[i];
+      if (at + i * kCopyThreads < page_vecs) __stcs(dst + at + i * kCopyThreads, x[i]);
   }
 }
 

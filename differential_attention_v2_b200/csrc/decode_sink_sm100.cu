@@ -213,17 +213,25 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         }
         __syncwarp();
       }
-      float sacc[NT][4];
+      // two accumulators (even and odd K-steps): half the length of the chain of dependent MMAs
+      float sacc[NT][4], sodd[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sacc[nt][c] = sodd[nt][c] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const int chunk = 2 * kk + k_csel;
         uint32_t a0, a1, a2, a3;
         ldmatrix_x4(kb + (chunk >> 3) * kHalfBytes + k_row * 128 + (((chunk & 7) ^ (k_row & 7)) << 4), a0, a1, a2, a3);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_m16n8k16_bf16(sacc[nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
+        for (int nt = 0; nt < NT; ++nt)
+          mma_m16n8k16_bf16(kk & 1 ? sodd[nt] : sacc[nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sacc[nt][c] += sodd[nt][c];
       const int ta = tok + 16 * warp + gl;
       const bool va = !edge || seen(ta), vb8 = !edge || seen(ta + 8);
       uint32_t pb[NT][2];
@@ -370,11 +378,16 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   cl.sync();  // no CTA leaves while another reads its partial
 }
 
-// CTAs per (KV head, sequence): double while the GPU's SMs have none and a CTA keeps a stage, then
-// while there are fewer than eight waves of two CTAs per SM and a CTA keeps eight stages.
+// CTAs per (KV head, sequence): as many as fit the GPU at two CTAs per SM, but no more than there
+// are stages; 16 (a non-portable size, slow to place) only for long lists. Measured on B200 (us, 8
+// KV heads, 4 sinks; CTAs per cluster 1 / 2 / 4 / 8 / 16):
+//   B=1,  window 1024    16.6  11.3   8.6   7.7   8.8
+//   B=1,  window 32768    316   161    84    46    31
+//   B=8,  window 4096    45.6  27.9  26.6  32.5  56.3
+//   B=32, window 1024    28.5  33.4  45.4  71.4   162
 int cluster_size(long long units, int span) {
   int c = 1;
-  while (c < kMaxCluster && ((units * c < 148 && span >= 2 * c) || (units * c < 148 * 16 && span >= 16 * c))) c *= 2;
+  while (c < kMaxCluster && 2 * c * units <= 296 && span > c && (c < 8 || span >= 256)) c *= 2;
   return c;
 }
 

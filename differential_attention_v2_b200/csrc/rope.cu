@@ -9,12 +9,17 @@
 // (2c, 2c+1) when interleaved; dimensions from 2P on pass through. The rotation is orthogonal, so
 // its gradient is the rotation by -phi (`inverse`).
 //
-// Bound by HBM: every element is read and written once, 3 flops each. A CTA takes one token: it
-// issues its first loads of q and k (16 bytes per thread and half), computes the token's P angles
-// once for all heads while they are in flight, and then turns head after head from shared
-// cos/sin. The angle is formed in 64 bits (an integer position times a fp32 frequency needs up to
-// 55 bits; at position 1e5 a fp32 product is off by 1e-2 radians), reduced to a fraction of a
-// turn there, and only then rounded to fp32 for sincospif.
+// Bound by HBM: every element is read and written once, 3 flops each. A warp takes one token and a
+// run of its heads, and no thread waits for another: a lane owns the same N pairs of every head it
+// visits, so their cos and sin stay in registers (the lanes that own the same pairs of different
+// heads compute a share each and exchange them). Memory is kept busy by the number of warps: one
+// head per lane in flight at 40 warps an SM measured 97 us for 16,384 tokens of 64 + 8 bf16 heads
+// of 128 (604 MB, 6.23 TB/s, 0.96 of a plain copy), two heads at 32 warps 99.6, and a CTA per
+// token with the angles in shared memory 158 (it issued three times the instructions, and its
+// warps waited for one another). Append holds more addresses and runs 32 warps: 60 us for 8,192
+// tokens (336 MB, 5.6 TB/s). The angle is formed in 64 bits (an integer position times a fp32 frequency needs up to
+// 55 bits; at position 1e5 a fp32 product is off by 1e-2 radians), reduced to a fraction of a turn
+// there, and only then rounded to fp32 for sincospif.
 //
 // Append: k goes to the row of its page (token i of sequence b's n_b new ones is logical position
 // seqlens[b] - n_b + i) and v beside it, so that neither is written to a buffer in between.
@@ -25,159 +30,201 @@
 namespace da2 {
 namespace rope {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 2;  // units per thread in flight
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
   T v[N];
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f32(float x, float& y) { y = x; }
-__device__ __forceinline__ void from_f32(float x, __nv_bfloat16& y) { y = __float2bfloat16_rn(x); }
-
-// A unit is N pairs of one head (two vectors of N elements), or 2N of its dimensions that pass
-// through. Units of a head: P/N rotated ones, then (D - 2P)/(2N) others; a v head has D/(2N)
-// others.
-template <typename T, int N, bool kInter, bool kAppend>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  extern __shared__ float2 cs[];  // (cos, sin) of the token's P pairs
-  __shared__ int s_seq;
-  __shared__ long long s_row;
-  using V = Vec<T, N>;
-  const int t = blockIdx.x;
-  const int upr = p.P / N, uph = p.D / (2 * N);  // units per head: rotated, all
-  const int units = (p.Hq + p.Hkv * (kAppend ? 2 : 1)) * uph;
-
-  if (kAppend) {
-    if (p.cu_seqlens) {
-      if (threadIdx.x == 0) s_seq = -1;
-      __syncthreads();
-      for (int b = threadIdx.x; b < p.B; b += kThreads)
-        if (__ldg(p.cu_seqlens + b) <= t && t < __ldg(p.cu_seqlens + b + 1)) s_seq = b;
-      __syncthreads();
-      if (s_seq < 0) return;  // a row behind the last sequence
-    } else if (threadIdx.x == 0) {
-      s_seq = t;
-    }
-    if (threadIdx.x == 0) {
-      const int b = s_seq;
-      const int end = p.cu_seqlens ? __ldg(p.cu_seqlens + b + 1) : t + 1;
-      const int at = __ldg(p.seqlens + b) - (end - t);
-      s_row = -1;
-      if (at >= 0 && (at >> p.page_shift) < p.max_pages) {
-        const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (at >> p.page_shift));
-        if (page >= 0 && page < p.num_pages)
-          s_row = (static_cast<long long>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
-      }
+// The N elements of a vector in fp32, and back with one rounding.
+template <int N>
+__device__ __forceinline__ void unpack(const Vec<float, N>& a, float (&f)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = a.v[e];
+}
+template <int N>
+__device__ __forceinline__ void pack(const float (&f)[N], Vec<float, N>& a) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) a.v[e] = f[e];
+}
+template <int N>
+__device__ __forceinline__ void unpack(const Vec<__nv_bfloat16, N>& a, float (&f)[N]) {
+  if constexpr (N == 1) {
+    f[0] = __bfloat162float(a.v[0]);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&a);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      f[2 * e] = __uint_as_float(w[e] << 16);
+      f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
   }
-
-  // where a unit reads and writes; false past the last unit
-  auto place = [&](int u, const T*& lo, const T*& hi, T*& wlo, T*& whi, int& c) -> bool {
-    if (u >= units) return false;
-    const int h = u / uph, r = u - h * uph;
-    const T* src;
-    T* dst;
-    bool rot = r < upr;
-    if (h < p.Hq) {
-      src = static_cast<const T*>(p.q) + t * p.q_stride + static_cast<size_t>(h) * p.D;
-      dst = static_cast<T*>(p.q_out) + t * p.qo_stride + static_cast<size_t>(h) * p.D;
-    } else if (!kAppend || h < p.Hq + p.Hkv) {
-      const int hk = h - p.Hq;
-      src = static_cast<const T*>(p.k) + t * p.k_stride + static_cast<size_t>(hk) * p.D;
-      dst = kAppend ? static_cast<T*>(p.k_out) + static_cast<size_t>(hk) * p.D
-                    : static_cast<T*>(p.k_out) + t * p.ko_stride + static_cast<size_t>(hk) * p.D;
-    } else {
-      const int hk = h - p.Hq - p.Hkv;
-      src = static_cast<const T*>(p.v) + t * p.v_stride + static_cast<size_t>(hk) * p.D;
-      dst = static_cast<T*>(p.v_out) + static_cast<size_t>(hk) * p.D;
-      rot = false;
-    }
-    int a, b;
-    if (rot) {
-      c = r * N;
-      a = kInter ? 2 * c : c;
-      b = kInter ? 2 * c + N : p.P + c;
-    } else {
-      c = -1;
-      a = 2 * N * r;  // rotated units cover dimensions 0 .. 2P-1 = 2 N upr
-      b = a + N;
-    }
-    lo = src + a;
-    hi = src + b;
-    wlo = dst + a;
-    whi = dst + b;
-    return true;
-  };
-
-  bool first = true;
-  for (int base = 0; base < units; base += kThreads * kUnroll) {
-    V x[kUnroll], y[kUnroll];
-    T *wx[kUnroll], *wy[kUnroll];
-    int c[kUnroll];
-    bool ok[kUnroll];
+}
+template <int N>
+__device__ __forceinline__ void pack(const float (&f)[N], Vec<__nv_bfloat16, N>& a) {
+  if constexpr (N == 1) {
+    a.v[0] = __float2bfloat16_rn(f[0]);
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&a);
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const T *lo, *hi;
-      ok[i] = place(base + i * kThreads + static_cast<int>(threadIdx.x), lo, hi, wx[i], wy[i], c[i]);
-      if (ok[i]) {
-        x[i] = *reinterpret_cast<const V*>(lo);
-        y[i] = *reinterpret_cast<const V*>(hi);
-      }
+    for (int e = 0; e < N / 2; ++e) w[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+  }
+}
+
+// Logical position -> row of the paged cache for token t; -1: not stored, -2: not a token.
+__device__ __forceinline__ long long cache_row(const RopeParams& p, int t, int lane) {
+  int b = t, end = t + 1;
+  if (p.cu_seqlens) {
+    b = -1;
+    for (int b0 = 0; b0 < p.B && b < 0; b0 += 32) {
+      const int i = b0 + lane;
+      const bool in = i < p.B && __ldg(p.cu_seqlens + i) <= t && t < __ldg(p.cu_seqlens + i + 1);
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (m) b = b0 + __ffs(m) - 1;
     }
-    if (first) {
-      for (int j = threadIdx.x; j < p.P; j += kThreads) {
+    if (b < 0) return -2;  // behind the last sequence
+    end = __ldg(p.cu_seqlens + b + 1);
+  }
+  const int at = __ldg(p.seqlens + b) - (end - t);
+  if (at < 0 || (at >> p.page_shift) >= p.max_pages) return -1;
+  const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (at >> p.page_shift));
+  if (page < 0 || page >= p.num_pages) return -1;
+  return (static_cast<long long>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Heads h, h + step, .. < n of one tensor at element offsets off + h * D: turned, or copied.
+template <typename T, int N, bool kInter, bool kTurn>
+__device__ __forceinline__ void walk(const T* src, T* dst, int h, int step, int n, int D,
+                                     int ra, int rb, const float (&co)[N], const float (&si)[N]) {
+  using V = Vec<T, N>;
+  for (; h < n; h += step) {
+    V x = *reinterpret_cast<const V*>(src + h * D + ra);
+    V y = *reinterpret_cast<const V*>(src + h * D + rb);
+    if constexpr (kTurn) {
+      float a[N], b[N];
+      unpack(x, a);
+      unpack(y, b);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        // pair e of the unit: (a[e], b[e]), or neighbours when interleaved
+        float& fa = kInter ? (2 * e < N ? a[(2 * e) % N] : b[(2 * e) % N]) : a[e];
+        float& fb = kInter ? (2 * e + 1 < N ? a[(2 * e + 1) % N] : b[(2 * e + 1) % N]) : b[e];
+        const float u = fa * co[e] - fb * si[e];
+        fb = fb * co[e] + fa * si[e];
+        fa = u;
+      }
+      pack(a, x);
+      pack(b, y);
+    }
+    *reinterpret_cast<V*>(dst + h * D + ra) = x;
+    *reinterpret_cast<V*>(dst + h * D + rb) = y;
+  }
+}
+
+// Lane l works on unit r = l % per_head of head l / per_head of each step, per_head = min(units
+// per head, 32). A unit is N pairs of a head (two vectors of N elements), or 2N of its dimensions
+// that pass through: units 0 .. P/N-1 rotate, the rest and all of a v head are copied.
+template <typename T, int N, bool kInter, bool kAppend>
+__global__ void __launch_bounds__(kThreads, kAppend ? 8 : 10)
+rope_kernel(const RopeParams p, const int chunks, const int chunk_heads) {
+  const int lane = threadIdx.x & 31;
+  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int t = static_cast<int>(item / chunks);
+  if (t >= p.T) return;  // the whole warp
+  const int uph = p.D / (2 * N), upr = p.P / N;
+  const int per_head = min(uph, 32), hpw = 32 / per_head;
+  const int heads = p.Hq + p.Hkv * (kAppend ? 2 : 1);
+  const int h0 = static_cast<int>(item - static_cast<long long>(t) * chunks) * chunk_heads;
+  const int h1 = min(heads, h0 + chunk_heads);
+  const int hs = lane / per_head;  // hpw: this lane has no head (32 is not a multiple of per_head)
+  const size_t tt = static_cast<size_t>(t);
+
+  const T* q = static_cast<const T*>(p.q) + tt * p.q_stride;
+  // this lane's first head on its way to L2 while the angles are computed
+  if (h0 + hs < p.Hq) prefetch_l2(q + static_cast<size_t>(h0 + hs) * p.D + (lane % per_head) * N);
+  const long long row = kAppend ? cache_row(p, t, lane) : 0;
+  if (kAppend && row == -2) return;
+
+  for (int r0 = 0; r0 < uph; r0 += per_head) {
+    const int r = r0 + lane % per_head;
+    const bool rot = r < upr;
+    // cos and sin of the unit's pairs: in round j lane hs of a unit computes pair j * hpw + hs, and
+    // the unit's lanes exchange them
+    float co[N], si[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      co[e] = 1.f;
+      si[e] = 0.f;
+    }
+#pragma unroll 1
+    for (int j = 0; j * hpw < N; ++j) {
+      const int e0 = j * hpw + hs, c = r * N + e0;
+      float s = 0.f, k = 1.f;
+      if (rot && e0 < N) {
         int axis = 0;
-        while (axis + 1 < p.n_axes && j >= p.sec_end[axis]) ++axis;
+        while (axis + 1 < p.n_axes && c >= p.sec_end[axis]) ++axis;
         double turn = static_cast<double>(__ldg(p.positions + static_cast<size_t>(axis) * p.T + t)) *
-                      static_cast<double>(__ldg(p.inv_freq + j)) * 0.15915494309189535;
+                      static_cast<double>(__ldg(p.inv_freq + c)) * 0.15915494309189535;
         turn -= rint(turn);
-        float s, co;
-        sincospif(static_cast<float>(2.0 * turn), &s, &co);
-        cs[j] = make_float2(co, p.inverse ? -s : s);
+        sincospif(static_cast<float>(2.0 * turn), &s, &k);
+        if (p.inverse) s = -s;
       }
-      __syncthreads();
-      first = false;
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e >= j * hpw && e < (j + 1) * hpw) {
+          const int from = (e - j * hpw) * per_head + lane % per_head;
+          co[e] = __shfl_sync(0xffffffffu, k, from);
+          si[e] = __shfl_sync(0xffffffffu, s, from);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (!ok[i]) continue;
-      if (c[i] >= 0) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          // element e of the unit's N pairs: (x[e], y[e]), or neighbours when interleaved
-          T& a = kInter ? (2 * e < N ? x[i].v[(2 * e) % N] : y[i].v[(2 * e) % N]) : x[i].v[e];
-          T& b = kInter ? (2 * e + 1 < N ? x[i].v[(2 * e + 1) % N] : y[i].v[(2 * e + 1) % N]) : y[i].v[e];
-          const float2 r = cs[c[i] + e];
-          const float fa = to_f32(a), fb = to_f32(b);
-          from_f32(fa * r.x - fb * r.y, a);
-          from_f32(fb * r.x + fa * r.y, b);
-        }
-      }
-      size_t off = 0;
-      if (kAppend) {
-        const int h = (base + i * kThreads + static_cast<int>(threadIdx.x)) / uph;
-        if (h >= p.Hq) {
-          if (s_row < 0) continue;  // no page for this token: only its q is written
-          off = static_cast<size_t>(s_row) * p.Hkv * p.D;
-        }
-      }
-      *reinterpret_cast<V*>(wx[i] + off) = x[i];
-      *reinterpret_cast<V*>(wy[i] + off) = y[i];
+    const int ca = 2 * N * r, cb = ca + N;  // offsets of a unit that is copied
+    const int ra = rot && !kInter ? r * N : ca, rb = rot && !kInter ? p.P + r * N : cb;
+    const bool mine = hs < hpw && r < uph;
+    if (!mine) continue;
+    // this lane's heads of q, then k, then v among h0 + hs, h0 + hs + hpw, .. < h1
+    T* qo = static_cast<T*>(p.q_out) + tt * p.qo_stride;
+    const int nq = min(h1, p.Hq);
+    int h = h0 + hs;
+    // a unit that passes through has cos 1 and sin 0, but is copied: -0 and NaN keep their bits
+    if (rot) walk<T, N, kInter, true>(q, qo, h, hpw, nq, p.D, ra, rb, co, si);
+    else walk<T, N, kInter, false>(q, qo, h, hpw, nq, p.D, ra, rb, co, si);
+    if (h < p.Hq) h += (p.Hq - h + hpw - 1) / hpw * hpw;
+    if (h >= h1 || (kAppend && row < 0)) continue;  // (no page for this token: only its q is written)
+    const size_t at = kAppend ? static_cast<size_t>(row) * p.Hkv * p.D : tt * p.ko_stride;
+    const T* k = static_cast<const T*>(p.k) + tt * p.k_stride;
+    T* ko = static_cast<T*>(p.k_out) + at;
+    const int nk = min(h1 - p.Hq, p.Hkv);
+    if (rot) walk<T, N, kInter, true>(k, ko, h - p.Hq, hpw, nk, p.D, ra, rb, co, si);
+    else walk<T, N, kInter, false>(k, ko, h - p.Hq, hpw, nk, p.D, ra, rb, co, si);
+    if (kAppend) {
+      h -= p.Hq + p.Hkv;
+      if (h < 0) h += (-h + hpw - 1) / hpw * hpw;
+      walk<T, N, kInter, false>(static_cast<const T*>(p.v) + tt * p.v_stride, static_cast<T*>(p.v_out) + at, h, hpw,
+                                h1 - p.Hq - p.Hkv, p.D, ca, cb, co, si);
     }
   }
 }
 
 template <typename T, int N>
 cudaError_t launch_n(const RopeParams& p, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(p.P) * sizeof(float2);
   const bool append = p.block_table != nullptr;
+  const int uph = p.D / (2 * N), hpw = 32 / (uph < 32 ? uph : 32);
+  const int heads = p.Hq + p.Hkv * (append ? 2 : 1);
+  // One warp per token; with few tokens (decode steps) a token's heads are dealt to several warps,
+  // down to four heads per lane, until there are 8 warps for every SM.
+  const int steps = (heads + 4 * hpw - 1) / (4 * hpw);
+  int chunks = 1;
+  while (chunks < steps && static_cast<long long>(p.T) * chunks < 148 * 8) ++chunks;
+  const int chunk_heads = (steps + chunks - 1) / chunks * 4 * hpw;
+  chunks = (heads + chunk_heads - 1) / chunk_heads;
   auto kernel = append ? (p.interleaved ? rope_kernel<T, N, true, true> : rope_kernel<T, N, false, true>)
                        : (p.interleaved ? rope_kernel<T, N, true, false> : rope_kernel<T, N, false, false>);
-  kernel<<<p.T, kThreads, smem, stream>>>(p);
+  const long long items = static_cast<long long>(p.T) * chunks;
+  kernel<<<static_cast<unsigned>((items + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p, chunks, chunk_heads);
   return cudaGetLastError();
 }
 
