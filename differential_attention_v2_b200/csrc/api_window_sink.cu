@@ -66,7 +66,8 @@ int backward(const void* q, const void* k, const void* v, const float* lambda, c
   // grid limits: 128-row tiles on grid y; the preprocess runs 4 (row, pair) warps per CTA
   const long long padded = packed ? static_cast<long long>(total) + 128LL * B + 128
                                   : static_cast<long long>(B) * (static_cast<long long>(S) + 128);
-  if ((static_cast<long long>(S) + 127) / 128 > 65535 || padded > 2147483647LL ||
+  // (and the parts of the tiles that hold sinks beside them)
+  if ((static_cast<long long>(S) + 127) / 128 > 60000 || padded > 2147483647LL ||
       padded * (Hq / 2) > 4LL * 2147483647LL || static_cast<long long>(B) * Hq > 2147483647LL)
     return DA2_ERR_UNSUPPORTED;
   int* err = nullptr;
@@ -143,13 +144,13 @@ int diffattn_v2_prefill_varlen_window_sink_train(const void* q, const void* k, c
 
 size_t diffattn_v2_backward_window_sink_workspace_size(int B, int S, int Hq, int Hkv, int window, int sink) {
   if (B <= 0 || S <= 0 || !da2::paired_heads(Hq, Hkv) || window < 1 || sink < 0) return 0;
-  return da2::backward_stats_bytes(B, S, Hq);
+  return da2::backward_sink_workspace_bytes(B, S, 0, Hq, Hkv, window, sink, false);
 }
 
 size_t diffattn_v2_backward_varlen_window_sink_workspace_size(int B, int max_seqlen, int total_tokens, int Hq, int Hkv,
                                                               int window, int sink) {
   if (B <= 0 || max_seqlen <= 0 || total_tokens <= 0 || !da2::paired_heads(Hq, Hkv) || window < 1 || sink < 0) return 0;
-  return da2::backward_varlen_workspace_bytes(B, total_tokens, Hq);
+  return da2::backward_sink_workspace_bytes(B, max_seqlen, total_tokens, Hq, Hkv, window, sink, true);
 }
 
 int diffattn_v2_backward_window_sink(const void* q, const void* k, const void* v, const float* lambda,

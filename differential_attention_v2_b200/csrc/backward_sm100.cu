@@ -98,7 +98,58 @@ struct Params {
   const int* cu_seqlens;     // packed sequences: sequence b is rows cu[b] .. cu[b+1]-1 (null: [B,S])
   const int* pad_off;        // packed sequences: first row of sequence b in the row terms (128-aligned)
   float scale, scale_log2;
+  // kSink: how the dK/dV steps of a key tile are split (SinkPlan), fp32 partials [slot][dV, dK]
+  // [128 keys][128 d], and for packed sequences the first slot of each
+  int sink_tiles, sink_parts, tile_parts, part_steps;
+  float* partial;
+  const int* slot_off;
 };
+
+// With sinks the dK/dV work of a KV head is uneven: a tile that holds sinks is seen by every later
+// query block, a plain tile only by those of its window. The steps (pair, 64-row query block) of a
+// tile are therefore cut into parts of at most part_steps, a plain tile's own number (or, where the
+// whole launch is long, a quarter of an SM's share: finer parts balance nothing and cost their fp32
+// sums), each a CTA's work; sum_parts_kernel adds the parts of a tile in order. Where the whole grid
+// is less than half a wave, plain tiles are cut too.
+struct SinkPlan {
+  int sink_tiles;  // key tiles that hold sinks
+  int sink_parts;  // CTAs for one of them
+  int tile_parts;  // CTAs for a plain tile
+  int part_steps;
+  long long slots;  // fp32 partials that a launch may write
+};
+
+__host__ __device__ inline int parts_of(int steps, int most, int part_steps) {
+  const int n = (steps + part_steps - 1) / part_steps;
+  return n < 1 ? 1 : (n < most ? n : most);
+}
+
+// total: tokens of the launch; S: the longest sequence.
+SinkPlan sink_plan(int B, int S, long long total, int Hq, int Hkv, int window, int sink, bool packed) {
+  SinkPlan pl;
+  const long long gpairs = Hq / Hkv / 2, n_tiles = (S + 127) / 128, nq = (S + 63) / 64;
+  const long long plain = nq < window / 64 + 3LL ? nq : window / 64 + 3LL;  // query blocks of a plain tile
+  pl.sink_tiles = (sink < S ? sink + 127 : S + 127) / 128;
+  const long long ctas = B * n_tiles * Hkv;
+  const long long cut = ctas <= 74 ? 148 / ctas : 1;
+  const long long all = Hkv * gpairs * ((total / 64 + B) * pl.sink_tiles + (total / 128 + B) * plain);
+  long long len = (plain * gpairs + cut - 1) / cut;
+  if (len < all / (148 * 4)) len = all / (148 * 4);
+  if (len < 8) len = 8;
+  pl.part_steps = static_cast<int>(len < (1 << 24) ? len : 1 << 24);
+  const int most = parts_of(static_cast<int>(nq * gpairs), 1 << 24, pl.part_steps);
+  pl.sink_parts = pl.sink_tiles > 0 ? most : 1;
+  pl.tile_parts = static_cast<int>(cut < most ? cut : most);
+  // sequences of one part write no slot; one of n > 1 parts has more than (n - 1) part_steps steps
+  long long seq_slots = static_cast<long long>(B) * pl.sink_parts;
+  if (packed && pl.tile_parts == 1) {
+    const long long bound = 2 * (total / 64 + B) * gpairs / pl.part_steps + 2;
+    seq_slots = seq_slots < bound ? seq_slots : bound;
+  }
+  pl.slots = pl.sink_parts > 1 ? seq_slots * Hkv * pl.sink_tiles : 0;
+  if (pl.tile_parts > 1) pl.slots += static_cast<long long>(B) * Hkv * (n_tiles - pl.sink_tiles) * pl.tile_parts;
+  return pl;
+}
 
 // ------------------------------------------------------------------------ preprocess
 // Offset of row i's term k in the stats of (b, pair).
@@ -168,6 +219,38 @@ __global__ void pad_offsets_kernel(const int* __restrict__ cu, int* __restrict__
     }
     pad_off[B] = acc;
   }
+}
+
+// The same with sinks, and the first partial slot of each sequence (slot_off[b], in units of
+// Hkv * sink_tiles slots): one warp scans both.
+__global__ void pad_offsets_sink_kernel(const int* __restrict__ cu, int* __restrict__ pad_off,
+                                        int* __restrict__ slot_off, int B, int gpairs, int sink_parts,
+                                        int part_steps) {
+  const int lane = threadIdx.x;
+  int rows = 0, slots = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane;
+    const int n = b < B ? max(cu[b + 1] - cu[b], 0) : 0;
+    int r = (n + kRowPad - 1) / kRowPad * kRowPad;
+    const int parts = parts_of((n + 63) / 64 * gpairs, sink_parts, part_steps);
+    int s = parts > 1 ? parts : 0;
+    const int r0 = r, s0 = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, r, o), w = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) {
+        r += u;
+        s += w;
+      }
+    }
+    if (b < B) {
+      pad_off[b] = rows + r - r0;
+      slot_off[b] = slots + s - s0;
+    }
+    rows += __shfl_sync(0xffffffffu, r, 31);
+    slots += __shfl_sync(0xffffffffu, s, 31);
+  }
+  if (lane == 0) pad_off[B] = rows;
 }
 
 // The preprocess for packed sequences: warp w is padded row pr of pair p (rows of all pairs
@@ -314,6 +397,54 @@ __device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, fl
   }
 }
 
+// The same in fp32.
+__device__ __forceinline__ void store_row_f32(uint32_t taddr, float* dst, float mul) {
+#pragma unroll 1
+  for (int c = 0; c < 128 / kGroups / 32; ++c) {
+    uint32_t a[32];
+    tmem_ld_x32_wait(taddr + 32 * c, a);
+    float4* d = reinterpret_cast<float4*>(dst + 32 * c);
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      d[v] = make_float4(__uint_as_float(a[4 * v]) * mul, __uint_as_float(a[4 * v + 1]) * mul,
+                         __uint_as_float(a[4 * v + 2]) * mul, __uint_as_float(a[4 * v + 3]) * mul);
+  }
+}
+
+constexpr size_t kSlotFloats = 2 * 128 * HD;  // dV and dK of one tile
+
+// Key tile and part of CTA y of a sequence's KV head: the sink tiles' parts, then the plain tiles'.
+__device__ __forceinline__ void dkdv_tile(const Params& p, int y, int& tile, int& part) {
+  const int n_sink = p.sink_tiles * p.sink_parts;
+  if (y < n_sink) {
+    tile = y / p.sink_parts;
+    part = y - tile * p.sink_parts;
+  } else {
+    tile = (y - n_sink) / p.tile_parts;
+    part = y - n_sink - tile * p.tile_parts;
+    tile += p.sink_tiles;
+  }
+}
+
+// The slot of a split tile's part: the sequences' sink tiles first, then the plain tiles.
+template <bool kVarlen>
+__device__ __forceinline__ size_t partial_slot(const Params& p, int b, int g, int tile, int part, int parts) {
+  if (tile < p.sink_tiles) {
+    // a sequence has room for the parts of its first tile, its longest
+    int first = b * p.sink_parts, room = p.sink_parts;
+    if (kVarlen) {
+      const int n = __ldg(p.cu_seqlens + b + 1) - __ldg(p.cu_seqlens + b);
+      first = __ldg(p.slot_off + b);
+      room = parts_of((n + 63) / 64 * (p.Hq / p.Hkv / 2), p.sink_parts, p.part_steps);
+    }
+    return (static_cast<size_t>(first) * p.Hkv + static_cast<size_t>(g) * room) * p.sink_tiles +
+           static_cast<size_t>(tile) * room + part;
+  }
+  const size_t base = p.sink_parts > 1 ? static_cast<size_t>(p.B) * p.sink_parts * p.Hkv * p.sink_tiles : 0;
+  return base + ((static_cast<size_t>(b) * p.Hkv + g) * (p.n_tiles - p.sink_tiles) + (tile - p.sink_tiles)) *
+                    p.tile_parts + part;
+}
+
 // N (kCols) consecutive fp32 columns of this warp's 32 lanes; the wait completes them.
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
@@ -387,7 +518,9 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   const int n_pairs = p.Hq >> 1, group = p.Hq / p.Hkv, gpairs = group >> 1;
   const int g = static_cast<int>(blockIdx.x) % p.Hkv;
   const int b = static_cast<int>(blockIdx.x) / p.Hkv;
-  const int tile = static_cast<int>(blockIdx.y);  // tile 0 (most query blocks when causal) first
+  int tile = static_cast<int>(blockIdx.y);  // tile 0 (most query blocks when causal) first
+  int part = 0;
+  if constexpr (kSink) dkdv_tile(p, static_cast<int>(blockIdx.y), tile, part);
   const int k0 = tile * 128;
   // sequence extent: a [B,S] batch, or packed sequences whose tensors are one [1,T] batch
   // (tok0: the sequence's first row; tb: the batch coordinate of the tensor maps; sb, srow0:
@@ -409,7 +542,15 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   // (a tile with sinks by every later query)
   const int q_end = kWindow && !(kSink && k0 < p.sink) ? min(nq, (k0 + 126 + p.window) / 64 + 1) : nq;
   const int steps_per_pair = q_end - q_first;
-  const int n_steps = gpairs * steps_per_pair;
+  int n_steps = gpairs * steps_per_pair;
+  // kSink: this CTA's part of the tile's steps (step0 .. step0 + n_steps - 1)
+  int step0 = 0, parts = 1;
+  if constexpr (kSink) {
+    parts = parts_of(n_steps, tile < p.sink_tiles ? p.sink_parts : p.tile_parts, p.part_steps);
+    if (part >= parts) return;  // uniform over the CTA
+    step0 = static_cast<int>(static_cast<long long>(n_steps) * part / parts);
+    n_steps = static_cast<int>(static_cast<long long>(n_steps) * (part + 1) / parts) - step0;
+  }
 
   const uint32_t tmem = setup(bar0, tmem_slot, abort_flag, warp);
 
@@ -427,8 +568,8 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       for (int t = 0; t < n_steps; ++t) {
         const int s = t & 1;
         if (!mbar_wait(bar(kXEmpty + s), ((t >> 1) & 1) ^ 1, abort_flag)) break;
-        const int pair = g * gpairs + t / steps_per_pair;
-        const int q0 = (q_first + t % steps_per_pair) * 64;
+        const int pair = g * gpairs + (step0 + t) / steps_per_pair;
+        const int q0 = (q_first + (step0 + t) % steps_per_pair) * 64;
         const uint32_t st = sbase + kKvOffX + s * kKvStage;
         mbar_arrive_expect_tx(bar(kXFull + s), 3 * kStreamTile + kStatBytes);
         for (int c = 0; c < 2; ++c) {
@@ -531,7 +672,7 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     }
     for (int t = 0; ok && t < n_steps; ++t) {
       const int s = t & 1;
-      const int q0 = (q_first + t % steps_per_pair) * 64;
+      const int q0 = (q_first + (step0 + t) % steps_per_pair) * 64;
       ok = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + cg / kGroupsPerChain), t & 1, abort_flag));
       // the stage's stat records came by bulk copy: observe its completion directly (the
       // stage is refilled only after this step's operands have been consumed)
@@ -611,11 +752,59 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       // rows of the whole launch: B x S, or the packed sequences' total
       const size_t total_rows = kVarlen ? static_cast<size_t>(__ldg(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
       const bool valid = key < S && checked(off + 128 / kGroups <= total_rows * p.Hkv * HD, p.err);
-      store_row(trow + kTmAcc0 + d0, p.dv + off, 1.f, valid);
-      store_row(trow + kTmAcc1 + d0, p.dk + off, p.scale, valid);
+      if (kSink && parts > 1) {
+        float* dst = p.partial + partial_slot<kVarlen>(p, b, g, tile, part, parts) * kSlotFloats + r * HD + d0;
+        store_row_f32(trow + kTmAcc0 + d0, dst, 1.f);
+        store_row_f32(trow + kTmAcc1 + d0, dst + kSlotFloats / 2, p.scale);
+      } else {
+        store_row(trow + kTmAcc0 + d0, p.dv + off, 1.f, valid);
+        store_row(trow + kTmAcc1 + d0, p.dk + off, p.scale, valid);
+      }
     }
   }
   teardown(tmem, abort_flag, p.err, warp);
+}
+
+// Adds the parts of the split key tiles, in order, and rounds once. Bound by HBM and launch latency:
+// blockIdx = (KV head of a sequence, tile, 16 of its rows), a thread takes 4 float4.
+constexpr int kSumThreads = 256;
+template <bool kVarlen>
+__global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const Params p) {
+  const int g = static_cast<int>(blockIdx.x) % p.Hkv, b = static_cast<int>(blockIdx.x) / p.Hkv;
+  const int tile = static_cast<int>(blockIdx.y), k0 = tile * 128;
+  int S = p.S, tok0 = 0;
+  size_t row_base = static_cast<size_t>(b) * p.S;
+  if (kVarlen) {
+    tok0 = __ldg(p.cu_seqlens + b);
+    S = __ldg(p.cu_seqlens + b + 1) - tok0;
+    row_base = static_cast<size_t>(tok0);
+  }
+  const int r0 = k0 + 16 * static_cast<int>(blockIdx.z);
+  if (r0 >= S) return;
+  const int nq = (S + 63) / 64, q_first = k0 / 64;
+  const int q_end = k0 < p.sink ? nq : min(nq, (k0 + 126 + p.window) / 64 + 1);
+  const int parts = parts_of((q_end - q_first) * (p.Hq / p.Hkv / 2), tile < p.sink_tiles ? p.sink_parts : p.tile_parts,
+                             p.part_steps);
+  if (parts == 1) return;
+  const float* src = p.partial + partial_slot<kVarlen>(p, b, g, tile, 0, parts) * kSlotFloats;
+#pragma unroll
+  for (int i = 0; i < 2 * 16 * HD / 4 / kSumThreads; ++i) {
+    const int u = i * kSumThreads + threadIdx.x;  // which of dV, dK; row; float4 of the row
+    const int which = u / (16 * HD / 4), row = u / (HD / 4) % 16, c = u % (HD / 4);
+    const float* at = src + which * (kSlotFloats / 2) + (r0 - k0 + row) * HD + 4 * c;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int q = 0; q < parts; ++q) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(at + q * kSlotFloats));
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    if (r0 + row < S)
+      *reinterpret_cast<uint2*>((which ? p.dk : p.dv) + ((row_base + r0 + row) * p.Hkv + g) * HD + 4 * c) =
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
 }
 
 // --------------------------------------------------------------------------------- dQ
@@ -856,6 +1045,23 @@ static size_t varlen_stat_rows(int B, int T) {
          bwd_tc::kRowPad * bwd_tc::kRowPad;
 }
 
+// Row terms, (packed) padded offsets and first slots, then the partials.
+static size_t sink_slots_offset(int B, int S, int T, int Hq, bool packed) {
+  if (!packed) return (backward_stats_bytes(B, S, Hq) + 15) / 16 * 16;
+  return backward_varlen_workspace_bytes(B, T, Hq) + (static_cast<size_t>(B) + 3) / 4 * 16;
+}
+
+size_t backward_sink_workspace_bytes(int B, int S, int T, int Hq, int Hkv, int window, int sink, bool packed) {
+  if (window >= S || sink >= S) {  // the causal mask
+    window = S;
+    sink = 0;
+  }
+  const bwd_tc::SinkPlan pl =
+      bwd_tc::sink_plan(B, S, packed ? T : static_cast<long long>(B) * S, Hq, Hkv, window, sink, packed);
+  return sink_slots_offset(B, S, T, Hq, packed) +
+         static_cast<size_t>(pl.slots) * bwd_tc::kSlotFloats * sizeof(float);
+}
+
 size_t backward_varlen_workspace_bytes(int B, int T, int Hq) {
   const size_t stats = static_cast<size_t>(Hq / 2) * varlen_stat_rows(B, T) * bwd_tc::kStatArrays * sizeof(float);
   return stats + (static_cast<size_t>(B) + 1 + 3) / 4 * 16;  // + the B+1 padded offsets
@@ -873,11 +1079,29 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   const int n_pairs = Hq / 2;
   Params p;
   cudaError_t e;
+  SinkPlan plan = {};
+  if (o_branch_f32) {
+    // the sink form; window <= 0: every earlier key, the causal mask
+    if (window <= 0) {
+      window = S;
+      sink = 0;
+    }
+    plan = sink_plan(B, S, cu_seqlens ? total_tokens : static_cast<long long>(B) * S, Hq, Hkv, window, sink,
+                     cu_seqlens != nullptr);
+  }
   if (cu_seqlens) {
     // S is the longest sequence; the row terms of all sequences form one padded batch
     const int S_pad = static_cast<int>(varlen_stat_rows(B, total_tokens));
     int* pad_off = reinterpret_cast<int*>(workspace + static_cast<size_t>(n_pairs) * S_pad * kStatArrays);
-    pad_offsets_kernel<<<1, 32, 0, stream>>>(cu_seqlens, pad_off, B);
+    if (o_branch_f32) {
+      int* slot_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(workspace) +
+                                             backward_varlen_workspace_bytes(B, total_tokens, Hq));
+      pad_offsets_sink_kernel<<<1, 32, 0, stream>>>(cu_seqlens, pad_off, slot_off, B, Hq / Hkv / 2, plan.sink_parts,
+                                                    plan.part_steps);
+      p.slot_off = slot_off;
+    } else {
+      pad_offsets_kernel<<<1, 32, 0, stream>>>(cu_seqlens, pad_off, B);
+    }
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long warps = static_cast<long long>(S_pad) * n_pairs;
@@ -933,10 +1157,31 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     return cudaGetLastError();
   };
   if (o_branch_f32) {
-    // the sink form (window >= S: every earlier key, the causal mask)
-    if (window <= 0) p.window = S;
-    return cu_seqlens ? run(dkdv_sm100<true, true, true>, dq_sm100<true, true, true>)
-                      : run(dkdv_sm100<false, true, true>, dq_sm100<false, true, true>);
+    p.sink_tiles = plan.sink_tiles;
+    p.sink_parts = plan.sink_parts;
+    p.tile_parts = plan.tile_parts;
+    p.part_steps = plan.part_steps;
+    p.partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
+                                         sink_slots_offset(B, S, total_tokens, Hq, cu_seqlens != nullptr));
+    const int tile_ctas = plan.sink_tiles * plan.sink_parts + (p.n_tiles - plan.sink_tiles) * plan.tile_parts;
+    auto run_sink = [&](auto kdkdv, auto ksum, auto kdq) {
+      cudaError_t r = cudaFuncSetAttribute(kdkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
+      if (r != cudaSuccess) return r;
+      r = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem);
+      if (r != cudaSuccess) return r;
+      kdkdv<<<dim3(B * Hkv, tile_ctas), kThreads, kKvSmem, stream>>>(tmQ64, tmO64, tmK128, tmV128, p);
+      r = cudaGetLastError();
+      if (r != cudaSuccess) return r;
+      kdq<<<dim3(B * n_pairs, p.n_tiles), kThreads, kQSmem, stream>>>(tmQ128, tmO128, tmK64, tmV64, p);
+      r = cudaGetLastError();
+      if (r != cudaSuccess) return r;
+      // only the tiles that may have been split
+      const int split_tiles = plan.tile_parts > 1 ? p.n_tiles : (plan.sink_parts > 1 ? plan.sink_tiles : 0);
+      if (split_tiles > 0) ksum<<<dim3(B * Hkv, split_tiles, 128 / 16), kSumThreads, 0, stream>>>(p);
+      return cudaGetLastError();
+    };
+    return cu_seqlens ? run_sink(dkdv_sm100<true, true, true>, sum_parts_kernel<true>, dq_sm100<true, true, true>)
+                      : run_sink(dkdv_sm100<false, true, true>, sum_parts_kernel<false>, dq_sm100<false, true, true>);
   }
   if (cu_seqlens && window > 0) return run(dkdv_sm100<true, true>, dq_sm100<true, true>);
   if (cu_seqlens) return run(dkdv_sm100<true, false>, dq_sm100<true, false>);

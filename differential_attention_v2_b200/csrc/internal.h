@@ -52,6 +52,8 @@ cudaError_t launch_prefill_lambda_fused(const CUtensorMap& tmQ, const CUtensorMa
 // o_branch_f32 the sink form: keys 0 .. sink-1 too (o_branch unused).
 size_t backward_stats_bytes(int B, int S, int Hq);
 size_t backward_varlen_workspace_bytes(int B, int T, int Hq);
+// the sink form's workspace (T: total tokens of packed sequences)
+size_t backward_sink_workspace_bytes(int B, int S, int T, int Hq, int Hkv, int window, int sink, bool packed);
 cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& tmQ128, const CUtensorMap& tmO64,
                                   const CUtensorMap& tmO128, const CUtensorMap& tmK64, const CUtensorMap& tmK128,
                                   const CUtensorMap& tmV64, const CUtensorMap& tmV128, const float* lambda,
