@@ -11,7 +11,7 @@ says how to build it.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -90,6 +90,8 @@ def load(path=LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    # addresses of the entry points that are called through the native half
+    lib.addresses = {name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _SIGNATURES}
     return lib
 
 
@@ -105,6 +107,28 @@ class DiffAttnError(RuntimeError):
 def _check(status: int, what: str):
     if status != OK:
         raise DiffAttnError(status, what)
+
+
+def _load_native():
+    path = os.path.join(_PKG, "_native.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing; build it with `python -m differential_attention_v2_b200.build`")
+    spec = importlib.util.spec_from_file_location(__package__ + "._native", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.on_error(_check)
+    return module
+
+
+_native = _load_native()
+_invoke = _native.invoke
+
+
+def _entry(name, description):
+    """An entry point of short calls: the native half checks its tensors, allocates the outputs that
+    are not given and calls it on their device and the given or current stream, as described (see
+    csrc/binding.cpp for the notation)."""
+    return _native.define(name, description)
 
 
 def _stream(stream, device):
@@ -227,12 +251,8 @@ def prefill_window(q, k, v, lam, window, out=None, stream=None, sink=None):
     """bf16 causal prefill where query i sees only keys i-window+1 .. i, and with `sink` the
     first `sink` keys too."""
     if sink is not None:
-        device, (B, S, Hq, D) = _shape(q, "q", 4)
-        Hkv = _attention_inputs(q, k, v, lam, device)
-        out = _new(out, "out", torch.bfloat16, (B, S, Hq // 2, D), device, stream)
-        _call("diffattn_v2_prefill_window_sink", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-              lam.data_ptr(), out.data_ptr(), B, S, Hq, Hkv, D, int(window), int(sink))
-        return out
+        return _invoke(_PREFILL_SINK, LIB.addresses["diffattn_v2_prefill_window_sink"], q, k, v, lam, window, sink, out,
+                       stream)
     for t, n, nd in ((q, "q", 4), (k, "k", 4), (v, "v", 4)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 3)
@@ -271,14 +291,8 @@ def prefill_varlen_window(q, k, v, lam, cu_seqlens, max_seqlen, window, out=None
     of a sequence sees that sequence's keys i-window+1 .. i, and with `sink` its first `sink`
     keys too."""
     if sink is not None:
-        device, (T, Hq, D) = _shape(q, "q", 3)
-        Hkv = _attention_inputs(q, k, v, lam, device)
-        B = _sequences(cu_seqlens, device)
-        out = _new(out, "out", torch.bfloat16, (T, Hq // 2, D), device, stream)
-        _call("diffattn_v2_prefill_varlen_window_sink", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-              lam.data_ptr(), out.data_ptr(), cu_seqlens.data_ptr(), B, int(max_seqlen), T, Hq, Hkv, D, int(window),
-              int(sink))
-        return out
+        return _invoke(_PREFILL_VARLEN_SINK, LIB.addresses["diffattn_v2_prefill_varlen_window_sink"], q, k, v, lam,
+                       cu_seqlens, max_seqlen, window, sink, out, stream)
     for t, n, nd in ((q, "q", 3), (k, "k", 3), (v, "v", 3)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 2)
@@ -316,15 +330,8 @@ def prefill_train(q, k, v, lam, out=None, o_branch=None, lse=None, causal=True, 
     With `window` the causal sliding-window prefill (query i sees keys i-window+1 .. i); with
     `sink` besides, the first `sink` keys stay visible and o_branch is fp32."""
     if sink is not None:
-        window = _window_of_sink(window, causal)
-        device, (B, S, Hq, D) = _shape(q, "q", 4)
-        Hkv = _attention_inputs(q, k, v, lam, device)
-        out = _new(out, "out", torch.bfloat16, (B, S, Hq // 2, D), device, stream)
-        o_branch = _new(o_branch, "o_branch", torch.float32, (B, S, Hq, D), device, stream)
-        lse = _new(lse, "lse", torch.float32, (B, S, Hq), device, stream)
-        _call("diffattn_v2_prefill_window_sink_train", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-              lam.data_ptr(), out.data_ptr(), o_branch.data_ptr(), lse.data_ptr(), B, S, Hq, Hkv, D, window, int(sink))
-        return out, o_branch, lse
+        return _invoke(_TRAIN_SINK, LIB.addresses["diffattn_v2_prefill_window_sink_train"], q, k, v, lam,
+                       _window_of_sink(window, causal), sink, out, o_branch, lse, stream)
     for t, n, nd in ((q, "q", 4), (k, "k", 4), (v, "v", 4)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 3)
@@ -425,17 +432,8 @@ def prefill_varlen_train(q, k, v, lam, cu_seqlens, max_seqlen, out=None, o_branc
     (out [T,Hq/2,D], o_branch [T,Hq,D], lse [T,Hq]). With `window` the causal sliding window
     inside every sequence."""
     if sink is not None:  # with a window: the first `sink` keys stay visible, o_branch fp32
-        window = _window_of_sink(window, causal)
-        device, (T, Hq, D) = _shape(q, "q", 3)
-        Hkv = _attention_inputs(q, k, v, lam, device)
-        B = _sequences(cu_seqlens, device)
-        out = _new(out, "out", torch.bfloat16, (T, Hq // 2, D), device, stream)
-        o_branch = _new(o_branch, "o_branch", torch.float32, (T, Hq, D), device, stream)
-        lse = _new(lse, "lse", torch.float32, (T, Hq), device, stream)
-        _call("diffattn_v2_prefill_varlen_window_sink_train", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-              lam.data_ptr(), out.data_ptr(), o_branch.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), B,
-              int(max_seqlen), T, Hq, Hkv, D, window, int(sink))
-        return out, o_branch, lse
+        return _invoke(_TRAIN_VARLEN_SINK, LIB.addresses["diffattn_v2_prefill_varlen_window_sink_train"], q, k, v, lam,
+                       cu_seqlens, max_seqlen, _window_of_sink(window, causal), sink, out, o_branch, lse, stream)
     for t, n, nd in ((q, "q", 3), (k, "k", 3), (v, "v", 3)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 2)
@@ -515,32 +513,13 @@ def decode_workspace_size(B, Smax, Hq, Hkv, D) -> int:
     return int(LIB.diffattn_v2_decode_workspace_size(B, Smax, Hq, Hkv, D))
 
 
-def _decode_inputs(q, kcache, vcache, seqlens, lam, window, lead):
-    """Checks the tensors of a decode step over caches [*lead, Hkv, D] (None: any extent)."""
-    if window is None:
-        raise ValueError("sink needs a window")
-    device, (B, Hq, D) = _shape(q, "q", 3)
-    if kcache.dim() != 4:
-        raise ValueError(f"cache: expected 4 dimensions, got shape {tuple(kcache.shape)}")
-    n, rows, Hkv, _ = kcache.shape
-    _expect(q, "q", torch.bfloat16, (B, Hq, D), device)
-    _expect(kcache, "K cache", torch.bfloat16, (n if lead is None else lead, rows, Hkv, D), device)
-    _expect(vcache, "V cache", torch.bfloat16, (n, rows, Hkv, D), device)
-    _expect(seqlens, "seqlens", torch.int32, (B,), device)
-    _expect(lam, "lam", torch.float32, (B, Hq // 2), device)
-    return device, B, Hq, Hkv, D, n, rows
-
-
 def decode(q, kcache, vcache, seqlens, lam, out=None, workspace=None, stream=None, window=None, sink=None):
     """bf16 decode step: q [B,Hq,D], caches [B,Smax,Hkv,D], seqlens int32 [B], lam fp32 [B,Hq/2].
     With `window` the new token sees only its sequence's last `window` keys, with `sink` besides
     the first `sink` ones (no workspace)."""
     if sink is not None:
-        device, B, Hq, Hkv, D, _, Smax = _decode_inputs(q, kcache, vcache, seqlens, lam, window, q.shape[0])
-        out = _new(out, "out", torch.bfloat16, (B, Hq // 2, D), device, stream)
-        _call("diffattn_v2_decode_window_sink", device, stream, q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
-              seqlens.data_ptr(), lam.data_ptr(), out.data_ptr(), B, Smax, Hq, Hkv, D, int(window), int(sink))
-        return out
+        return _invoke(_DECODE_SINK, LIB.addresses["diffattn_v2_decode_window_sink"], q, kcache, vcache, seqlens, lam,
+                       _window_of_sink(window, True), sink, out, stream)
     _need(q, "q", torch.bfloat16, 3)
     _need(kcache, "kcache", torch.bfloat16, 4)
     _need(vcache, "vcache", torch.bfloat16, 4)
@@ -597,13 +576,8 @@ def decode_paged(q, kpages, vpages, block_table, seqlens, lam, out=None, workspa
     the new token sees only its sequence's last `window` keys, with `sink` besides the first
     `sink` ones (no workspace; entries of pages without a visible key may be -1)."""
     if sink is not None:
-        device, B, Hq, Hkv, D, num_pages, page_size = _decode_inputs(q, kpages, vpages, seqlens, lam, window, None)
-        _expect(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), device)
-        out = _new(out, "out", torch.bfloat16, (B, Hq // 2, D), device, stream)
-        _call("diffattn_v2_decode_paged_window_sink", device, stream, q.data_ptr(), kpages.data_ptr(),
-              vpages.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), lam.data_ptr(), out.data_ptr(), B,
-              block_table.shape[1], page_size, num_pages, Hq, Hkv, D, int(window), int(sink))
-        return out
+        return _invoke(_DECODE_PAGED_SINK, LIB.addresses["diffattn_v2_decode_paged_window_sink"], q, kpages, vpages,
+                       block_table, seqlens, lam, _window_of_sink(window, True), sink, out, stream)
     _need(q, "q", torch.bfloat16, 3)
     _need(kpages, "kpages", torch.bfloat16, 4)
     _need(vpages, "vpages", torch.bfloat16, 4)
@@ -739,67 +713,14 @@ def decode_noalloc(q, kcache, vcache, seqlens, lam, out=None, stream=None):
     return out
 
 
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
-
-
-@functools.lru_cache(maxsize=64)
-def _sections(sections):
-    return (ctypes.c_int * len(sections))(*sections), len(sections), sum(sections)
-
-
-def _heads(t, name, dtype, T, D, device):
-    """[T, H, D] with the heads of a token contiguous; returns H and the token stride."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-        raise ValueError(f"{name}: expected shape [{T}, heads, {D}], got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
-    H = t.shape[1]
-    st, sh, sd = t.stride()
-    if sd != 1 or (sh != D and H > 1) or (st < H * D and T > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-    return H, st if T > 1 else H * D
-
-
-def _rope_inputs(q, positions, inv_freq, sections):
-    device, (T, _, D) = _shape(q, "q", 3)
-    if q.dtype not in _DTYPES:
-        raise TypeError(f"q: expected bfloat16 or float32, got {q.dtype}")
-    array, n_axes, pairs = _sections(tuple(sections))
-    _expect(positions, "positions", torch.int32, (n_axes, T), device)
-    _expect(inv_freq, "inv_freq", torch.float32, (pairs,), device)
-    Hq, q_stride = _heads(q, "q", q.dtype, T, D, device)
-    return device, T, D, Hq, q_stride, array, n_axes
-
-
 def rope(q, k, positions, inv_freq, sections, q_out=None, k_out=None, inverse=False, interleaved=False, stream=None):
     """Rotary positions with len(sections) axes (1 to 4): q [T,Hq,D], k [T,Hkv,D] or None, bf16 or
     fp32 (heads of a token contiguous, any token stride), positions int32 [n_axes, T], inv_freq
     fp32 [sum(sections)]; pair c turns by positions[axis(c)] * inv_freq[c]. Pairs are dimensions
     (c, c + P), interleaved (2c, 2c + 1); `inverse` turns back (the gradient). Outputs may be the
     inputs. Returns (q_out, k_out)."""
-    device, T, D, Hq, q_stride, array, n_axes = _rope_inputs(q, positions, inv_freq, sections)
-    dtype = q.dtype
-    if q_out is None:
-        q_out, qo_stride = _new(None, "q_out", dtype, (T, Hq, D), device, stream), Hq * D
-    else:
-        h, qo_stride = _heads(q_out, "q_out", dtype, T, D, device)
-        if h != Hq:
-            raise ValueError(f"q_out: expected {Hq} heads, got {h}")
-    Hkv = k_stride = ko_stride = 0
-    if k is not None:
-        Hkv, k_stride = _heads(k, "k", dtype, T, D, device)
-        if k_out is None:
-            k_out, ko_stride = _new(None, "k_out", dtype, (T, Hkv, D), device, stream), Hkv * D
-        else:
-            h, ko_stride = _heads(k_out, "k_out", dtype, T, D, device)
-            if h != Hkv:
-                raise ValueError(f"k_out: expected {Hkv} heads, got {h}")
-    _call("diffattn_v2_rope", device, stream, q.data_ptr(), _ptr(k), q_out.data_ptr(),
-          None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), array, n_axes, T, Hq, Hkv,
-          D, q_stride, k_stride, qo_stride, ko_stride, _DTYPES[dtype], 1 if interleaved else 0, 1 if inverse else 0)
-    return q_out, None if k is None else k_out
+    return _invoke(_ROPE, LIB.addresses["diffattn_v2_rope"], q, k, positions, inv_freq, sections, q_out, k_out, inverse,
+                   interleaved, stream)
 
 
 def rope_append_paged(q, k, v, positions, inv_freq, sections, kpages, vpages, block_table, seqlens, cu_seqlens=None,
@@ -810,126 +731,109 @@ def rope_append_paged(q, k, v, positions, inv_freq, sections, kpages, vpages, bl
     [num_pages, page_size, Hkv, D] of the same dtype; cu_seqlens int32 [B+1] tells the sequences'
     new tokens (None: one each). Rows of q_out behind the last sequence are not written. Returns
     q_out."""
-    device, T, D, Hq, q_stride, array, n_axes = _rope_inputs(q, positions, inv_freq, sections)
-    dtype = q.dtype
-    Hkv, k_stride = _heads(k, "k", dtype, T, D, device)
-    hv, v_stride = _heads(v, "v", dtype, T, D, device)
-    if kpages.dim() != 4 or hv != Hkv:
-        raise ValueError(f"caches [num_pages, page_size, {Hkv}, {D}] and v of {Hkv} heads are needed")
-    num_pages, page_size = kpages.shape[:2]
-    _expect(kpages, "kpages", dtype, (num_pages, page_size, Hkv, D), device)
-    _expect(vpages, "vpages", dtype, (num_pages, page_size, Hkv, D), device)
-    B = seqlens.numel() if cu_seqlens is None else _sequences(cu_seqlens, device)
-    _expect(seqlens, "seqlens", torch.int32, (B,), device)
-    _expect(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), device)
-    if q_out is None:
-        q_out, qo_stride = _new(None, "q_out", dtype, (T, Hq, D), device, stream), Hq * D
-    else:
-        h, qo_stride = _heads(q_out, "q_out", dtype, T, D, device)
-        if h != Hq:
-            raise ValueError(f"q_out: expected {Hq} heads, got {h}")
-    _call("diffattn_v2_rope_append_paged", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-          positions.data_ptr(), inv_freq.data_ptr(), array, n_axes, kpages.data_ptr(), vpages.data_ptr(),
-          block_table.data_ptr(), seqlens.data_ptr(), _ptr(cu_seqlens), T, B, block_table.shape[1], page_size,
-          num_pages, Hq, Hkv, D, q_stride, k_stride, v_stride, qo_stride, _DTYPES[dtype], 1 if interleaved else 0)
-    return q_out
+    return _invoke(_ROPE_APPEND, LIB.addresses["diffattn_v2_rope_append_paged"], q, k, v, positions, inv_freq, sections,
+                   kpages, vpages, block_table, seqlens, cu_seqlens, q_out, interleaved, stream)
 
 
-def _pool(block_table, refs, seqlens=None):
-    """Checks the state of a paged cache: block_table [B, max_pages], refs [num_pages], seqlens [B]."""
-    device, (B, max_pages) = _shape(block_table, "block_table", 2)
-    num_pages = refs.numel()
-    _expect(block_table, "block_table", torch.int32, (B, max_pages), device)
-    _expect(refs, "refs", torch.int32, (num_pages,), device)
-    if seqlens is not None:
-        _expect(seqlens, "seqlens", torch.int32, (B,), device)
-    return device, B, max_pages, num_pages
-
-
-def _result(given, device, stream, empty):
-    r = _new(given, "result", torch.int32, (1,), device, stream)
-    if empty:  # nothing is launched
-        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else torch.cuda.device(device):
-            r.zero_()
-    return r
+def _no_pages(result, block_table, n, stream):
+    """The result of a bookkeeping call on nothing, which launches nothing: 0."""
+    if n == 0 or block_table.shape[0] == 0:
+        if result is None:
+            result = torch.empty(1, dtype=torch.int32, device=block_table.device)
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+            result.zero_()
+    return result
 
 
 def cache_extend(block_table, seqlens, refs, n_new, page_size, result=None, stream=None):
     """n_new[b] more tokens for every sequence: seqlens grows and the pages that are missing are
     taken from the free ones (refs == 0), lowest first. Returns result int32 [1] on the device:
     pages taken, or -1 (too few free pages or a full row; nothing changed)."""
-    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
-    _expect(n_new, "n_new", torch.int32, (B,), device)
-    result = _result(result, device, stream, B == 0)
-    _call("diffattn_v2_cache_extend", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
-          n_new.data_ptr(), result.data_ptr(), B, max_pages, int(page_size), num_pages)
-    return result
+    result = _no_pages(result, block_table, 1, stream)
+    return _invoke(_CACHE_EXTEND, LIB.addresses["diffattn_v2_cache_extend"], block_table, seqlens, refs, n_new, page_size,
+                   result, stream)
 
 
 def cache_fork(block_table, seqlens, refs, parents, children, page_size, copies=None, result=None, stream=None):
     """Row children[i] (empty) continues what row parents[i] holds: whole pages are shared, a partly
     filled last page gets a page of its own. Returns (copies int32 [n,2] for cache_copy_pages, -1
     where there is none; result int32 [1]: pages taken, -1 too few free pages, -2 a bad pair)."""
-    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
-    n = parents.numel()
-    _expect(parents, "parents", torch.int32, (n,), device)
-    _expect(children, "children", torch.int32, (n,), device)
-    copies = _new(copies, "copies", torch.int32, (n, 2), device, stream)
-    if B == 0 and n > 0:
+    if block_table.shape[0] == 0 and parents.numel() > 0:
         raise ValueError("parents: the table has no rows")
-    result = _result(result, device, stream, n == 0)
-    _call("diffattn_v2_cache_fork", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
-          parents.data_ptr(), children.data_ptr(), copies.data_ptr(), result.data_ptr(), n, B, max_pages,
-          int(page_size), num_pages)
-    return copies, result
+    result = _no_pages(result, block_table, parents.numel(), stream)
+    return _invoke(_CACHE_FORK, LIB.addresses["diffattn_v2_cache_fork"], block_table, seqlens, refs, parents, children,
+                   page_size, copies, result, stream)
 
 
 def cache_trim(block_table, seqlens, refs, page_size, window, sink, result=None, stream=None):
     """Pages that hold neither one of the first `sink` keys nor one of the last `window` leave their
     sequence. Returns result int32 [1]: pages that became free."""
-    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
-    result = _result(result, device, stream, B == 0)
-    _call("diffattn_v2_cache_trim", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
-          result.data_ptr(), B, max_pages, int(page_size), num_pages, int(window), int(sink))
-    return result
+    result = _no_pages(result, block_table, 1, stream)
+    return _invoke(_CACHE_TRIM, LIB.addresses["diffattn_v2_cache_trim"], block_table, seqlens, refs, page_size, window,
+                   sink, result, stream)
 
 
 def cache_free(block_table, seqlens, refs, seqs, result=None, stream=None):
     """The listed sequences (int32; negative entries are padding) give their pages back and become
     empty. Returns result int32 [1]: pages that became free, or -2 (an index >= B; nothing changed)."""
-    device, B, max_pages, num_pages = _pool(block_table, refs, seqlens)
-    n = seqs.numel()
-    _expect(seqs, "seqs", torch.int32, (n,), device)
-    result = _result(result, device, stream, n == 0 or B == 0)
-    _call("diffattn_v2_cache_free", device, stream, block_table.data_ptr(), seqlens.data_ptr(), refs.data_ptr(),
-          seqs.data_ptr(), result.data_ptr(), n, B, max_pages, num_pages)
-    return result
+    result = _no_pages(result, block_table, seqs.numel(), stream)
+    return _invoke(_CACHE_FREE, LIB.addresses["diffattn_v2_cache_free"], block_table, seqlens, refs, seqs, result, stream)
 
 
 def cache_compact(block_table, refs, block_table_out=None, refs_out=None, moves=None, result=None, stream=None):
     """A plan that brings the L pages in use to the front of the pool. Returns (block_table, refs,
     moves int32 [num_pages // 2, 2] for cache_copy_pages, result int32 [1] = L); the outputs may be
     the inputs' own tensors."""
-    device, B, max_pages, num_pages = _pool(block_table, refs)
-    block_table_out = _new(block_table_out, "block_table_out", torch.int32, block_table.shape, device, stream)
-    refs_out = _new(refs_out, "refs_out", torch.int32, (num_pages,), device, stream)
-    moves = _new(moves, "moves", torch.int32, (num_pages // 2, 2), device, stream)
-    result = _new(result, "result", torch.int32, (1,), device, stream)
-    _call("diffattn_v2_cache_compact", device, stream, block_table.data_ptr(), refs.data_ptr(),
-          block_table_out.data_ptr(), refs_out.data_ptr(), moves.data_ptr(), result.data_ptr(), B, max_pages, num_pages)
-    return block_table_out, refs_out, moves, result
+    return _invoke(_CACHE_COMPACT, LIB.addresses["diffattn_v2_cache_compact"], block_table, refs, block_table_out,
+                   refs_out, moves, result, stream)
 
 
 def cache_copy_pages(kpages, vpages, copies, stream=None):
     """Copies page copies[i][0] to page copies[i][1] in both caches [num_pages, ...]; pairs with a
     negative entry are skipped. No page may be a destination twice, or a source and a destination."""
-    device = kpages.device
-    if not kpages.is_cuda or kpages.dim() < 2:
-        raise ValueError("kpages: must be a CUDA tensor [num_pages, ...]")
-    _expect(kpages, "kpages", kpages.dtype, kpages.shape, device)
-    _expect(vpages, "vpages", kpages.dtype, kpages.shape, device)
-    n = copies.shape[0]
-    _expect(copies, "copies", torch.int32, (n, 2), device)
-    num_pages = kpages.shape[0]
-    _call("diffattn_v2_cache_copy_pages", device, stream, kpages.data_ptr(), vpages.data_ptr(), copies.data_ptr(), n,
-          num_pages, kpages.numel() // max(num_pages, 1) * kpages.element_size())
+    _invoke(_CACHE_COPY, LIB.addresses["diffattn_v2_cache_copy_pages"], kpages, vpages, copies, stream)
+
+
+_BATCH = "q:bf16[B,S,Hq,D] k:bf16[B,S,Hkv,D] v:bf16[B,S,Hkv,D] lam:f32[B,S,Hq/2] "
+_PACKED = "q:bf16[T,Hq,D] k:bf16[T,Hkv,D] v:bf16[T,Hkv,D] lam:f32[T,Hq/2] cu_seqlens:i32[B+1] #max_seqlen "
+_POOL = "block_table:i32[B,max_pages] seqlens:i32[B] refs:i32[N] "
+_PREFILL_SINK = _entry("diffattn_v2_prefill_window_sink", _BATCH + """#window #sink >out:bf16[B,S,Hq/2,D]
+    -> q k v lam out B S Hq Hkv D window sink => out""")
+_PREFILL_VARLEN_SINK = _entry("diffattn_v2_prefill_varlen_window_sink", _PACKED + """#window #sink
+    >out:bf16[T,Hq/2,D] -> q k v lam out cu_seqlens B max_seqlen T Hq Hkv D window sink => out""")
+_TRAIN_SINK = _entry("diffattn_v2_prefill_window_sink_train", _BATCH + """#window #sink >out:bf16[B,S,Hq/2,D]
+    >o_branch:f32[B,S,Hq,D] >lse:f32[B,S,Hq] -> q k v lam out o_branch lse B S Hq Hkv D window sink
+    => out o_branch lse""")
+_TRAIN_VARLEN_SINK = _entry("diffattn_v2_prefill_varlen_window_sink_train", _PACKED + """#window #sink
+    >out:bf16[T,Hq/2,D] >o_branch:f32[T,Hq,D] >lse:f32[T,Hq]
+    -> q k v lam out o_branch lse cu_seqlens B max_seqlen T Hq Hkv D window sink => out o_branch lse""")
+_DECODE_SINK = _entry("diffattn_v2_decode_window_sink", """q:bf16[B,Hq,D] kcache:bf16[B,Smax,Hkv,D]
+    vcache:bf16[B,Smax,Hkv,D] seqlens:i32[B] lam:f32[B,Hq/2] #window #sink >out:bf16[B,Hq/2,D]
+    -> q kcache vcache seqlens lam out B Smax Hq Hkv D window sink => out""")
+_DECODE_PAGED_SINK = _entry("diffattn_v2_decode_paged_window_sink", """q:bf16[B,Hq,D] kpages:bf16[N,ps,Hkv,D]
+    vpages:bf16[N,ps,Hkv,D] block_table:i32[B,max_pages] seqlens:i32[B] lam:f32[B,Hq/2] #window #sink
+    >out:bf16[B,Hq/2,D] -> q kpages vpages block_table seqlens lam out B max_pages ps N Hq Hkv D window sink => out""")
+_ROPE = _entry("diffattn_v2_rope", """q:io<T,Hq,D> k:io<T,Hkv,D>? positions:i32[%.n,T] inv_freq:f32[%.sum] %sections
+    >q_out:io<T,Hq,D> >k_out:io<T,Hkv,D>?k !inverse !interleaved
+    -> q k q_out k_out positions inv_freq % %.n T Hq Hkv D q.s k.s q_out.s k_out.s io interleaved inverse
+    => q_out k_out""")
+_ROPE_APPEND = _entry("diffattn_v2_rope_append_paged", """q:io<T,Hq,D> k:io<T,Hkv,D> v:io<T,Hkv,D>
+    positions:i32[%.n,T] inv_freq:f32[%.sum] %sections kpages:io[N,ps,Hkv,D] vpages:io[N,ps,Hkv,D]
+    block_table:i32[B,max_pages] seqlens:i32[B] cu_seqlens:i32[B+1]? >q_out:io<T,Hq,D> !interleaved
+    -> q k v q_out positions inv_freq % %.n kpages vpages block_table seqlens cu_seqlens T B max_pages ps N Hq Hkv D
+    q.s k.s v.s q_out.s io interleaved => q_out""")
+_CACHE_EXTEND = _entry("diffattn_v2_cache_extend", _POOL + """n_new:i32[B] #page_size >result:i32[1]
+    -> block_table seqlens refs n_new result B max_pages page_size N => result""")
+_CACHE_FORK = _entry("diffattn_v2_cache_fork", _POOL + """parents:i32[n] children:i32[n] #page_size >copies:i32[n,2]
+    >result:i32[1] -> block_table seqlens refs parents children copies result n B max_pages page_size N
+    => copies result""")
+_CACHE_TRIM = _entry("diffattn_v2_cache_trim", _POOL + """#page_size #window #sink >result:i32[1]
+    -> block_table seqlens refs result B max_pages page_size N window sink => result""")
+_CACHE_FREE = _entry("diffattn_v2_cache_free", _POOL + """seqs:i32[n] >result:i32[1]
+    -> block_table seqlens refs seqs result n B max_pages N => result""")
+_CACHE_COMPACT = _entry("diffattn_v2_cache_compact", """block_table:i32[B,max_pages] refs:i32[N]
+    >block_table_out:i32[B,max_pages] >refs_out:i32[N] >moves:i32[N/2,2] >result:i32[1]
+    -> block_table refs block_table_out refs_out moves result B max_pages N
+    => block_table_out refs_out moves result""")
+_CACHE_COPY = _entry("diffattn_v2_cache_copy_pages", """kpages:any[N,...] vpages:any[N,...] copies:i32[n,2]
+    -> kpages vpages copies n N kpages.size =>""")

@@ -10,6 +10,9 @@ runs on machines without a GPU. Rebuilds only when a source is newer than the li
 -DDA2_DEBUG_BOUNDS, in which the kernels check their shared-memory, tensor-memory and global
 indices against the extents they address and report a violation through the device error
 word (code 4) instead of making the access. The tests load it directly.
+
+The library's Python binding has a native half, _native.so (csrc/binding.cpp, compiled with g++
+against torch's headers), which the same command builds.
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB_NAME = "libdiffattn_v2.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(PKG, "libdiffattn_v2_debug.so")
+NATIVE_PATH = os.path.join(PKG, "_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -61,6 +67,8 @@ def nvcc() -> str:
 def build(force: bool = False, verbose: bool = False, extra_flags=None, debug_bounds: bool = False) -> str:
     """Build the library (or, with debug_bounds, its bounds-checking twin); returns its path."""
     out = DEBUG_LIB_PATH if debug_bounds else LIB_PATH
+    if not debug_bounds:
+        build_native(force=force, verbose=verbose)
     if debug_bounds:
         extra_flags = list(extra_flags or []) + ["-DDA2_DEBUG_BOUNDS"]
     if not force and up_to_date(out):
@@ -76,6 +84,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug_bo
         print(res.stdout + res.stderr)
     os.replace(tmp, out)
     return out
+
+
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """Build _native.so, the native half of the Python binding (g++ against torch's headers)."""
+    made_from = (NATIVE_SOURCE, os.path.abspath(__file__))
+    if not force and os.path.exists(NATIVE_PATH) and all(
+            os.path.getmtime(p) <= os.path.getmtime(NATIVE_PATH) for p in made_from):
+        return NATIVE_PATH
+    import torch
+
+    torch_dir = os.path.dirname(torch.__file__)
+    include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [x for p in include for x in ("-isystem", p)] + [NATIVE_SOURCE, "-o", tmp, "-L", os.path.join(torch_dir, "lib")]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, NATIVE_PATH)
+    return NATIVE_PATH
 
 
 def main(argv=None):
