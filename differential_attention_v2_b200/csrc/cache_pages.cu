@@ -505,7 +505,9 @@ cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int
   e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return e;
   const long long items = static_cast<long long>(n) * 2 * pieces;
-  const long long most = 8LL * n_sms;  // 2048 threads an SM
+  // Many short-lived CTAs: 994 pages of 128 KB in both caches took 80 us (521 MB, 6.5 TB/s) with 64 CTAs
+  // for every SM, 95 with the 8 that are resident at a time.
+  const long long most = 64LL * n_sms;
   pages::copy_kernel<<<static_cast<unsigned>(items < most ? items : most), pages::kCopyThreads, 0, stream>>>(
       static_cast<uint4*>(k), static_cast<uint4*>(v), reinterpret_cast<const int2*>(copies), n, num_pages, page_vecs,
       pieces);

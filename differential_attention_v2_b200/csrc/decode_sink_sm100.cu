@@ -91,6 +91,18 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  if (threadIdx.x == 32 * kConsumerWarps) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmK8);
+    tma_prefetch_desc(&tmV8);
+  }
+  // the lambda of the first pair that this warp will write, on its way meanwhile
+  const int n_pairs = p.Hq >> 1;
+  const size_t pair0 = static_cast<size_t>(b) * n_pairs + g * (group / 2);
+  const int my_pair = rank + ctas * warp;
+  const float lam0 = my_pair < group / 2 ? __ldg(p.lambda + pair0 + my_pair) : 0.f;
+
   // visible keys: [0, ns) and [lo, n); stages 0 .. n_head-1 and from first_w on
   const int n = min(max(__ldg(p.seqlens + b), 0), p.Smax);
   const int lo = max(0, n - p.window);
@@ -335,13 +347,12 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   cl.sync();
 
   // Pair i of the group goes to warp (i / ctas) of CTA i % ctas; a lane takes 4 of d.
-  const int n_pairs = p.Hq >> 1;
   bool aborted = false;
   for (int r = 0; r < ctas; ++r) aborted |= *cl.map_shared_rank(const_cast<int*>(abort_flag), r) != 0;
   if (aborted) {
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kErrDecodeWait);
   } else {
-    for (int i = rank + ctas * warp; i < group / 2; i += ctas * (kConsumerWarps + 1)) {
+    for (int i = my_pair; i < group / 2; i += ctas * (kConsumerWarps + 1)) {
       float res[2][4];
 #pragma unroll
       for (int br = 0; br < 2; ++br) {
@@ -366,8 +377,8 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         res[br][2] = __fmul_rn(acc.z, inv);
         res[br][3] = __fmul_rn(acc.w, inv);
       }
-      const size_t row = static_cast<size_t>(b) * n_pairs + g * (group / 2) + i;
-      const float lam = __ldg(p.lambda + row);
+      const size_t row = pair0 + i;
+      const float lam = i == my_pair ? lam0 : __ldg(p.lambda + row);
       uint2 packed;
       packed.x = pack_bf16x2(__fmaf_rn(-lam, res[1][0], res[0][0]), __fmaf_rn(-lam, res[1][1], res[0][1]));
       packed.y = pack_bf16x2(__fmaf_rn(-lam, res[1][2], res[0][2]), __fmaf_rn(-lam, res[1][3], res[0][3]));
