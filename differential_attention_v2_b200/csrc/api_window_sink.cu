@@ -99,12 +99,12 @@ int decode(const void* q, const void* kcache, const void* vcache, const int32_t*
   int* err = nullptr;
   if (da2::device_error_word(&err) != cudaSuccess) return DA2_ERR_CUDA;
   const int rows = block_table ? 1 << page_shift : Smax, batch = block_table ? num_pages : B;
-  CUtensorMap tk, tv, tk8, tv8;
-  const uint32_t box = static_cast<uint32_t>(block_table && rows < 64 ? rows : 64);
-  if (!map(&tk, kcache, Hkv, rows, batch, box) || !map(&tv, vcache, Hkv, rows, batch, box) ||
-      !map(&tk8, kcache, Hkv, rows, batch, 8) || !map(&tv8, vcache, Hkv, rows, batch, 8))
+  CUtensorMap tk, tv;
+  const uint32_t tokens = block_table && rows < 16 ? 8 : 16;
+  if (da2::encode_kv_halves(&tk, kcache, Hkv, rows, batch, tokens) != cudaSuccess ||
+      da2::encode_kv_halves(&tv, vcache, Hkv, rows, batch, tokens) != cudaSuccess)
     return DA2_ERR_CUDA;
-  return status_of(da2::launch_decode_sink(tk, tv, tk8, tv8, static_cast<const bf16*>(q), seqlens, lambda,
+  return status_of(da2::launch_decode_sink(tk, tv, static_cast<const bf16*>(q), seqlens, lambda,
                                            static_cast<bf16*>(out), err, B, Smax, Hq, Hkv,
                                            window < Smax ? window : Smax, sink < Smax ? sink : Smax, block_table,
                                            max_pages, page_shift, reinterpret_cast<cudaStream_t>(stream)));

@@ -74,13 +74,16 @@ cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const 
                           cudaStream_t stream, int window = 0);
 
 // bf16 decode step (D = 128) over the last `window` and the first `sink` keys of each sequence:
-// one cluster per (KV head, sequence), no workspace. tmK, tmV as for launch_decode; tmK8, tmV8 the
-// same with boxes of 8 tokens.
-cudaError_t launch_decode_sink(const CUtensorMap& tmK, const CUtensorMap& tmV, const CUtensorMap& tmK8,
-                               const CUtensorMap& tmV8, const __nv_bfloat16* q, const int32_t* seqlens,
-                               const float* lambda, __nv_bfloat16* out, int* err, int B, int Smax, int Hq, int Hkv,
-                               int window, int sink, const int32_t* block_table, int max_pages, int page_shift,
-                               cudaStream_t stream);
+// one cluster per (KV head, sequence), no workspace. tmK, tmV from encode_kv_halves over the cache
+// (boxes of 16 tokens) or the pages (boxes of min(page_size, 16) tokens).
+cudaError_t launch_decode_sink(const CUtensorMap& tmK, const CUtensorMap& tmV, const __nv_bfloat16* q,
+                               const int32_t* seqlens, const float* lambda, __nv_bfloat16* out, int* err, int B,
+                               int Smax, int Hq, int Hkv, int window, int sink, const int32_t* block_table,
+                               int max_pages, int page_shift, cudaStream_t stream);
+
+// 5-D bf16 tensor map over a row-major [B,S,H,128] cache as (64 of d, token, half of d, head, b), box
+// {64, tokens, 2, 1, 1}, 128-byte swizzle: one copy brings both halves of a token run of one head.
+cudaError_t encode_kv_halves(CUtensorMap* map, const void* base, uint64_t H, uint64_t S, uint64_t B, uint32_t tokens);
 
 // Page bookkeeping of a paged cache (cache_pages.cu): one cluster each; block tables
 // [B, max_pages], refs [num_pages]; result one int. At most kMaxCacheSeqs sequences (extend) or
