@@ -157,20 +157,8 @@ __host__ __device__ __forceinline__ size_t stat_index(size_t bp, int S_pad, int 
   return (bp * (S_pad / kStatBlock) + i / kStatBlock) * (kStatArrays * kStatBlock) + k * kStatBlock + i % kStatBlock;
 }
 
-// Four consecutive values of a head's O_b row, bf16 or (with sinks) fp32.
-__device__ __forceinline__ float4 load_o4(const __nv_bfloat16* o, int lane) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(o) + lane);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ float4 load_o4(const float* o, int lane) {
-  return __ldg(reinterpret_cast<const float4*>(o) + lane);
-}
-
-template <typename TO>
 __global__ void __launch_bounds__(128)
-preprocess_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __restrict__ o_branch,
+preprocess_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ o_branch,
                   const float* __restrict__ lse, const float* __restrict__ lambda, float* __restrict__ stats,
                   float* __restrict__ dlam, int B, int S, int S_pad, int n_pairs) {
   const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -192,8 +180,10 @@ preprocess_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __restrict__
   float e[2];
 #pragma unroll
   for (int br = 0; br < 2; ++br) {
-    const float4 o = load_o4(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD, lane);
-    float v = g0.x * o.x + g0.y * o.y + g1.x * o.z + g1.y * o.w;
+    const uint2 o = __ldg(reinterpret_cast<const uint2*>(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD) + lane);
+    const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
+    const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
+    float v = g0.x * o0.x + g0.y * o0.y + g1.x * o1.x + g1.y * o1.y;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     e[br] = v;
@@ -256,9 +246,8 @@ __global__ void pad_offsets_sink_kernel(const int* __restrict__ cu, int* __restr
 // The preprocess for packed sequences: warp w is padded row pr of pair p (rows of all pairs
 // laid out as one batch of S_pad rows). Rows past a sequence's end, and past the padded
 // total, get -lse = -inf.
-template <typename TO>
 __global__ void __launch_bounds__(128)
-preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __restrict__ o_branch,
+preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bfloat16* __restrict__ o_branch,
                          const float* __restrict__ lse, const float* __restrict__ lambda, float* __restrict__ stats,
                          float* __restrict__ dlam, const int* __restrict__ cu, const int* __restrict__ pad_off, int B,
                          int S_pad, int n_pairs) {
@@ -286,8 +275,10 @@ preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __res
   float e[2];
 #pragma unroll
   for (int br = 0; br < 2; ++br) {
-    const float4 o = load_o4(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD, lane);
-    float v = g0.x * o.x + g0.y * o.y + g1.x * o.z + g1.y * o.w;
+    const uint2 o = __ldg(reinterpret_cast<const uint2*>(o_branch + (row * (2 * n_pairs) + 2 * p + br) * HD) + lane);
+    const float2 o0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
+    const float2 o1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
+    float v = g0.x * o0.x + g0.y * o0.y + g1.x * o1.x + g1.y * o1.y;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     e[br] = v;
@@ -300,6 +291,94 @@ preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const TO* __res
     stats[stat_index(p, S_pad, pr, lane)] = t;
   }
   if (lane == 0) dlam[row * n_pairs + p] = -e[1];
+}
+
+// The preprocess of the sink form (fp32 O_b). A CTA takes a 64-row record block of one pair; a warp
+// takes eight rows, four at a time (dO 8 bytes and O_1, O_2 16 bytes per lane and row in flight), and
+// the block's record leaves as 1280 consecutive bytes. Bound by HBM: dO and O_b are read once. With
+// one warp per row (above) 1 x 4096 tokens of 32 heads took 21.6 us.
+template <bool kVarlen>
+__global__ void __launch_bounds__(256)
+preprocess_sink_kernel(const __nv_bfloat16* __restrict__ dout, const float* __restrict__ o_branch,
+                       const float* __restrict__ lse, const float* __restrict__ lambda, float* __restrict__ stats,
+                       float* __restrict__ dlam, const int* __restrict__ cu, const int* __restrict__ pad_off, int B,
+                       int S, int S_pad, int n_pairs) {
+  __shared__ float rec[kStatArrays * kStatBlock];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = S_pad / kStatBlock;
+  // neighbouring CTAs: the pairs of the same rows
+  const int pair = static_cast<int>(blockIdx.x % n_pairs);
+  const long long rb = blockIdx.x / n_pairs;
+  const int blk = static_cast<int>(rb % blocks);
+  int b = static_cast<int>(rb / blocks);
+  const size_t bp = static_cast<size_t>(b) * n_pairs + pair;
+  // first row of the block within its sequence, the sequence's length and first row
+  int i0 = blk * kStatBlock, n = S;
+  size_t base = static_cast<size_t>(b) * S;
+  if (kVarlen) {
+    // the last sequence whose padded rows start at or before the block (b = B: behind all)
+    int lo = 0, hi = B;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(pad_off + mid) <= i0) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    n = 0;
+    base = 0;
+    if (b < B) {
+      i0 -= __ldg(pad_off + b);
+      base = static_cast<size_t>(__ldg(cu + b));
+      n = __ldg(cu + b + 1) - static_cast<int>(base);
+    }
+  }
+#pragma unroll
+  for (int r0 = 0; r0 < 8; r0 += 4) {
+    uint2 g[4];
+    float4 o[4][2];
+    bool ok[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 8 * warp + r0 + u;
+      ok[u] = i < n;
+      const size_t row = base + (ok[u] ? i : 0);
+      if (ok[u]) {
+        g[u] = __ldcs(reinterpret_cast<const uint2*>(dout + (row * n_pairs + pair) * HD) + lane);
+        const float4* ob = reinterpret_cast<const float4*>(o_branch + (row * n_pairs + pair) * 2 * HD);
+        o[u][0] = __ldcs(ob + lane);
+        o[u][1] = __ldcs(ob + HD / 4 + lane);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 8 * warp + r0 + u, at = 8 * warp + r0 + u;
+      float e[2] = {0.f, 0.f};
+      if (ok[u]) {
+        const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g[u].x));
+        const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g[u].y));
+#pragma unroll
+        for (int br = 0; br < 2; ++br) {
+          float v = g0.x * o[u][br].x + g0.y * o[u][br].y + g1.x * o[u][br].z + g1.y * o[u][br].w;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+          e[br] = v;
+        }
+      }
+      const size_t row = base + (ok[u] ? i : 0);
+      if (lane < kStatArrays) {
+        float t = lane < 2 ? -INFINITY : 0.f;  // a row past the sequence
+        if (ok[u]) {
+          if (lane < 2) t = -__ldg(lse + (row * n_pairs + pair) * 2 + lane);
+          else if (lane < 4) t = -e[lane - 2];
+          else t = -__ldg(lambda + row * n_pairs + pair);
+        }
+        rec[lane * kStatBlock + at] = t;
+      }
+      if (lane == 0 && ok[u]) dlam[row * n_pairs + pair] = -e[1];
+    }
+  }
+  __syncthreads();
+  float* dst = stats + stat_index(kVarlen ? pair : bp, S_pad, blk * kStatBlock, 0);
+  for (int i = threadIdx.x; i < kStatArrays * kStatBlock; i += 256) dst[i] = rec[i];
 }
 
 // Shared-memory layouts (byte offsets from a 1024-aligned base). Both tile kernels hold
@@ -502,10 +581,10 @@ __device__ __forceinline__ void tile_to_tmem(uint32_t tile, uint32_t trow, int r
 // kVarlen: packed sequences (p.cu_seqlens); kWindow: causal sliding window (p.window). The
 // plain [B,S] backward is the <false, false> instance and carries neither.
 // kSink (with kWindow): keys 0 .. p.sink-1 stay visible to every later query.
-template <bool kVarlen, bool kWindow, bool kSink = false>
-__global__ void __launch_bounds__(kThreads, 1)
-dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+// (bx, by): (KV head of a sequence, key tile), with sinks (the same, tile or part of one).
+template <bool kVarlen, bool kWindow, bool kSink>
+__device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
+                                         const CUtensorMap& tmV, const Params& p, int bx, int by) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -516,11 +595,11 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_pairs = p.Hq >> 1, group = p.Hq / p.Hkv, gpairs = group >> 1;
-  const int g = static_cast<int>(blockIdx.x) % p.Hkv;
-  const int b = static_cast<int>(blockIdx.x) / p.Hkv;
-  int tile = static_cast<int>(blockIdx.y);  // tile 0 (most query blocks when causal) first
+  const int g = bx % p.Hkv;
+  const int b = bx / p.Hkv;
+  int tile = by;  // tile 0 (most query blocks when causal) first
   int part = 0;
-  if constexpr (kSink) dkdv_tile(p, static_cast<int>(blockIdx.y), tile, part);
+  if constexpr (kSink) dkdv_tile(p, by, tile, part);
   const int k0 = tile * 128;
   // sequence extent: a [B,S] batch, or packed sequences whose tensors are one [1,T] batch
   // (tok0: the sequence's first row; tb: the batch coordinate of the tensor maps; sb, srow0:
@@ -765,6 +844,14 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   teardown(tmem, abort_flag, p.err, warp);
 }
 
+template <bool kVarlen, bool kWindow>
+__global__ void __launch_bounds__(kThreads, 1)
+dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+  dkdv_cta<kVarlen, kWindow, false>(tmQ, tmO, tmK, tmV, p, static_cast<int>(blockIdx.x),
+                                    static_cast<int>(blockIdx.y));
+}
+
 // Adds the parts of the split key tiles, in order, and rounds once. Bound by HBM and launch latency:
 // blockIdx = (KV head of a sequence, tile, 16 of its rows), a thread takes 4 float4.
 constexpr int kSumThreads = 256;
@@ -808,10 +895,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const Params p) 
 }
 
 // --------------------------------------------------------------------------------- dQ
-template <bool kVarlen, bool kWindow, bool kSink = false>
-__global__ void __launch_bounds__(kThreads, 1)
-dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
-         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+// (bx, by): (pair of a sequence, query tile from the last when causal)
+template <bool kVarlen, bool kWindow, bool kSink>
+__device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap& tmO, const CUtensorMap& tmK,
+                                       const CUtensorMap& tmV, const Params& p, int bx, int by) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -822,10 +909,10 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_pairs = p.Hq >> 1, group = p.Hq / p.Hkv;
-  const int pair = static_cast<int>(blockIdx.x) % n_pairs;
-  const int b = static_cast<int>(blockIdx.x) / n_pairs;
+  const int pair = bx % n_pairs;
+  const int b = bx / n_pairs;
   const int g = (2 * pair) / group;
-  const int tile = p.causal ? p.n_tiles - 1 - static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.y);
+  const int tile = p.causal ? p.n_tiles - 1 - by : by;
   const int m0 = tile * 128;
   // sequence extent, as in the dK/dV kernel
   int S = p.S, tok0 = 0, tb = b, srow0 = 0;
@@ -1032,6 +1119,33 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
   teardown(tmem, abort_flag, p.err, warp);
 }
 
+template <bool kVarlen, bool kWindow>
+__global__ void __launch_bounds__(kThreads, 1)
+dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+         const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+  dq_cta<kVarlen, kWindow, false>(tmQ, tmO, tmK, tmV, p, static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y));
+}
+
+// The sink form's tile kernels as one launch: n_kv CTAs of dK/dV, then those of dQ, which fill the
+// SMs that the last wave of the first leaves idle (both take a whole SM; a window makes their
+// numbers small: 280 and 512 CTAs for 4096 tokens).
+template <bool kVarlen>
+__global__ void __launch_bounds__(kThreads, 1)
+backward_sink_sm100(const __grid_constant__ CUtensorMap tmQ64, const __grid_constant__ CUtensorMap tmO64,
+                    const __grid_constant__ CUtensorMap tmK128, const __grid_constant__ CUtensorMap tmV128,
+                    const __grid_constant__ CUtensorMap tmQ128, const __grid_constant__ CUtensorMap tmO128,
+                    const __grid_constant__ CUtensorMap tmK64, const __grid_constant__ CUtensorMap tmV64,
+                    const Params p, const int n_kv) {
+  const int i = static_cast<int>(blockIdx.x);
+  if (i < n_kv) {
+    const int per = p.B * p.Hkv;
+    dkdv_cta<kVarlen, true, true>(tmQ64, tmO64, tmK128, tmV128, p, i % per, i / per);
+  } else {
+    const int per = p.B * (p.Hq >> 1), j = i - n_kv;
+    dq_cta<kVarlen, true, true>(tmQ128, tmO128, tmK64, tmV64, p, j % per, j / per);
+  }
+}
+
 }  // namespace bwd_tc
 
 size_t backward_stats_bytes(int B, int S, int Hq) {
@@ -1105,25 +1219,23 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long warps = static_cast<long long>(S_pad) * n_pairs;
-    const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
     if (o_branch_f32)
-      preprocess_varlen_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch_f32, lse, lambda, workspace, dlambda,
-                                                           cu_seqlens, pad_off, B, S_pad, n_pairs);
+      preprocess_sink_kernel<true><<<static_cast<unsigned>(warps / kStatBlock), 256, 0, stream>>>(
+          dout, o_branch_f32, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S, S_pad, n_pairs);
     else
-      preprocess_varlen_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch, lse, lambda, workspace, dlambda, cu_seqlens,
-                                                           pad_off, B, S_pad, n_pairs);
+      preprocess_varlen_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
+          dout, o_branch, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S_pad, n_pairs);
     p.S_pad = S_pad;
     p.pad_off = pad_off;
   } else {
     const int S_pad = (S + kRowPad - 1) / kRowPad * kRowPad;
     const long long warps = static_cast<long long>(B) * S_pad * n_pairs;
-    const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
     if (o_branch_f32)
-      preprocess_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch_f32, lse, lambda, workspace, dlambda, B, S, S_pad,
-                                                    n_pairs);
+      preprocess_sink_kernel<false><<<static_cast<unsigned>(warps / kStatBlock), 256, 0, stream>>>(
+          dout, o_branch_f32, lse, lambda, workspace, dlambda, nullptr, nullptr, B, S, S_pad, n_pairs);
     else
-      preprocess_kernel<<<blocks, 128, 0, stream>>>(dout, o_branch, lse, lambda, workspace, dlambda, B, S, S_pad,
-                                                    n_pairs);
+      preprocess_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
+          dout, o_branch, lse, lambda, workspace, dlambda, B, S, S_pad, n_pairs);
     p.S_pad = S_pad;
     p.pad_off = nullptr;
   }
@@ -1164,15 +1276,12 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     p.partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
                                          sink_slots_offset(B, S, total_tokens, Hq, cu_seqlens != nullptr));
     const int tile_ctas = plan.sink_tiles * plan.sink_parts + (p.n_tiles - plan.sink_tiles) * plan.tile_parts;
-    auto run_sink = [&](auto kdkdv, auto ksum, auto kdq) {
-      cudaError_t r = cudaFuncSetAttribute(kdkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, kKvSmem);
+    const int n_kv = B * Hkv * tile_ctas, n_ctas = n_kv + B * n_pairs * p.n_tiles;
+    auto run_sink = [&](auto ktiles, auto ksum) {
+      constexpr uint32_t smem = kKvSmem > kQSmem ? kKvSmem : kQSmem;
+      cudaError_t r = cudaFuncSetAttribute(ktiles, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (r != cudaSuccess) return r;
-      r = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize, kQSmem);
-      if (r != cudaSuccess) return r;
-      kdkdv<<<dim3(B * Hkv, tile_ctas), kThreads, kKvSmem, stream>>>(tmQ64, tmO64, tmK128, tmV128, p);
-      r = cudaGetLastError();
-      if (r != cudaSuccess) return r;
-      kdq<<<dim3(B * n_pairs, p.n_tiles), kThreads, kQSmem, stream>>>(tmQ128, tmO128, tmK64, tmV64, p);
+      ktiles<<<n_ctas, kThreads, smem, stream>>>(tmQ64, tmO64, tmK128, tmV128, tmQ128, tmO128, tmK64, tmV64, p, n_kv);
       r = cudaGetLastError();
       if (r != cudaSuccess) return r;
       // only the tiles that may have been split
@@ -1180,8 +1289,8 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
       if (split_tiles > 0) ksum<<<dim3(B * Hkv, split_tiles, 128 / 16), kSumThreads, 0, stream>>>(p);
       return cudaGetLastError();
     };
-    return cu_seqlens ? run_sink(dkdv_sm100<true, true, true>, sum_parts_kernel<true>, dq_sm100<true, true, true>)
-                      : run_sink(dkdv_sm100<false, true, true>, sum_parts_kernel<false>, dq_sm100<false, true, true>);
+    return cu_seqlens ? run_sink(backward_sink_sm100<true>, sum_parts_kernel<true>)
+                      : run_sink(backward_sink_sm100<false>, sum_parts_kernel<false>);
   }
   if (cu_seqlens && window > 0) return run(dkdv_sm100<true, true>, dq_sm100<true, true>);
   if (cu_seqlens) return run(dkdv_sm100<true, false>, dq_sm100<true, false>);
