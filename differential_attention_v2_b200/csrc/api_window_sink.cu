@@ -175,6 +175,7 @@ int diffattn_v2_decode_window_sink(const void* q, const void* kcache, const void
                                    const float* lambda, void* out, int B, int Smax, int Hq, int Hkv, int D, int window,
                                    int sink, da2_stream_t stream) {
   if (B < 0 || Smax <= 0 || D <= 0 || !da2::paired_heads(Hq, Hkv) || window < 1 || sink < 0) return DA2_ERR_INVALID;
+  if (Smax > (1 << 30)) return DA2_ERR_INVALID;
   if (B == 0) return DA2_OK;
   return decode(q, kcache, vcache, nullptr, seqlens, lambda, out, B, Smax, 0, 0, 0, Hq, Hkv, D, window, sink, stream);
 }

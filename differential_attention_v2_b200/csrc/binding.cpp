@@ -274,6 +274,11 @@ struct Call {
       const Dim& d = it.dims[i];
       if (d.sym >= 0 && !bound[d.sym]) {
         if (d.div != 1 || sizes[i] < d.add) return shape_error(it, t);
+        if (sizes[i] > INT32_MAX) {
+          PyErr_Format(PyExc_ValueError, "%s: a size of %lld does not fit 32 bits", it.name.c_str(),
+                       static_cast<long long>(sizes[i]));
+          return false;
+        }
         val[d.sym] = sizes[i] - d.add;
         bound[d.sym] = true;
       } else if (sizes[i] != want(d)) {

@@ -515,7 +515,8 @@ DA2_API int diffattn_v2_backward_varlen_window_sink(const void* q, const void* k
  * may overlap. Every visible K/V row is read once. Rows that are not visible may hold anything,
  * NaN included, and block-table entries of pages without a visible key are not read (they may be
  * -1 or name a page of another sequence); the entry of a page with a visible key must be in
- * [0, num_pages). An empty sequence gets zeros. Supported: D == 128, Hq/Hkv in {2, 4, 8, 16}.
+ * [0, num_pages). An empty sequence gets zeros. Supported: D == 128, Hq/Hkv in {2, 4, 8, 16}, caches
+ * of at most 2^30 tokens per sequence.
  */
 DA2_API int diffattn_v2_decode_window_sink(const void* q, const void* kcache, const void* vcache,
                                            const int32_t* seqlens, const float* lambda, void* out, int B, int Smax,
