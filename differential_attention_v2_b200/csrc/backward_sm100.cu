@@ -26,6 +26,8 @@
 // bf16 operands back over them. A step's scores are produced in two 32-column halves so that
 // the elementwise work on one half overlaps the MMAs of the other.
 
+#include <type_traits>
+
 #include "bounds.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -94,6 +96,7 @@ struct Params {
   int B, S, S_pad, Hq, Hkv, causal;
   int window;                // causal sliding window: query i sees keys i-window+1 .. i (0: none)
   int sink;                  // with a window: keys 0 .. sink-1 stay visible (kSink instances)
+  int fine_keys;             // kSink: dS of key blocks that start below this is two bf16 terms
   int n_tiles;               // 128-row tiles
   const int* cu_seqlens;     // packed sequences: sequence b is rows cu[b] .. cu[b+1]-1 (null: [B,S])
   const int* pad_off;        // packed sequences: first row of sequence b in the row terms (128-aligned)
@@ -571,6 +574,11 @@ __device__ __forceinline__ void st_packed(uint32_t taddr, const uint32_t (&r)[N]
   }
 }
 
+// What rounding (a, b) to the bf16 pair `packed` left, rounded in turn.
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t packed) {
+  return pack_bf16x2(a - __uint_as_float(packed << 16), b - __uint_as_float(packed & 0xFFFF0000u));
+}
+
 // Copy this thread's share of a resident 128-row K-major SW128 tile (row r = TMEM lane)
 // into TMEM from column kTmA on, as packed bf16 pairs along d (element 2j in the low half
 // of column j): the A-operand layout of a TS MMA. Each column group takes 128 / kGroups d.
@@ -945,6 +953,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
   const int n_head = kSink ? min((p.sink + 63) / 64, kb_first) : 0;
   const int n_steps = (p.causal ? min(nk, (m0 + 128) / 64) : nk) - kb_first + n_head;
   auto key_block = [&](int t) -> int { return kSink && t < n_head ? t : kb_first + t - n_head; };
+  // Sink keys resemble one another (that is how every query finds them), so the roundings of their dS
+  // add up along their common direction in dQ instead of averaging out: their blocks enter the
+  // product as two bf16 terms. With bf16 alone dQ was off by 3 to 4e-3 where 1.7e-3 is its own
+  // rounding; a block more costs 16 MMAs.
+  auto holds_sinks = [&](int t) -> bool { return kSink && 64 * key_block(t) < p.fine_keys; };
 
   const uint32_t tmem = setup(bar0, tmem_slot, abort_flag, warp);
 
@@ -1025,6 +1038,15 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
             mma_bf16_ts(tmem + kTmAcc0, tmem + kTmS1 + col, b_k, kIdescAcc, first);
             mma_bf16_ts(tmem + kTmAcc1, tmem + kTmS2 + col, b_k, kIdescAcc, first);
           }
+          if (kSink && holds_sinks(t)) {  // what the operands' rounding left
+#pragma unroll 1
+            for (int row = kChainCols * c; row < kChainCols * (c + 1); row += 16) {
+              const uint32_t col = operand_col(row) + kCols / 2;
+              const uint64_t b_k = desc_mnmajor(sK, kStreamChunk, row);
+              mma_bf16_ts(tmem + kTmAcc0, tmem + kTmS1 + col, b_k, kIdescAcc, 1u);
+              mma_bf16_ts(tmem + kTmAcc1, tmem + kTmS2 + col, b_k, kIdescAcc, 1u);
+            }
+          }
           if (next) {
             if (c == 0 && !(ok = mbar_wait(bar(kXFull + (s ^ 1)), ((t + 1) >> 1) & 1, abort_flag))) break;
             tc_fence_after();
@@ -1084,34 +1106,52 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
       const bool wedge = kWindow && 64 * kb < m0 + 128 - p.window;
       const int lim = p.causal ? min(qi, S - 1) : S - 1;  // last key this row sees
       const int lo = qi - p.window + 1;                      // first key it sees with a window
-      uint32_t d1_pk[kCols / 2], d2_pk[kCols / 2];
+      // (kFineBlock: with what the rounding of the operands left; a copy of the code of its own, as a
+      // branch in every pair slowed all blocks)
+      auto elementwise = [&](auto fine_block) {
+        constexpr bool kFineBlock = decltype(fine_block)::value;
+        uint32_t d1_pk[kCols / 2], d2_pk[kCols / 2];
+        uint32_t d1_lo[kCols / 2], d2_lo[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 2) {
-        const uint64_t a1 = f2_fma(f2_pack(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])), sc2, nl1_2);
-        const uint64_t a2 = f2_fma(f2_pack(__uint_as_float(s2[c]), __uint_as_float(s2[c + 1])), sc2, nl2_2);
-        float x0, x1, y0, y1;
-        f2_unpack(a1, x0, x1);
-        f2_unpack(a2, y0, y1);
-        float p10 = fast_exp2(x0), p11 = fast_exp2(x1), p20 = fast_exp2(y0), p21 = fast_exp2(y1);
-        if (masked) {
-          if (kbase + c > lim) p10 = p20 = 0.f;
-          if (kbase + c + 1 > lim) p11 = p21 = 0.f;
+        for (int c = 0; c < kCols; c += 2) {
+          const uint64_t a1 = f2_fma(f2_pack(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])), sc2, nl1_2);
+          const uint64_t a2 = f2_fma(f2_pack(__uint_as_float(s2[c]), __uint_as_float(s2[c + 1])), sc2, nl2_2);
+          float x0, x1, y0, y1;
+          f2_unpack(a1, x0, x1);
+          f2_unpack(a2, y0, y1);
+          float p10 = fast_exp2(x0), p11 = fast_exp2(x1), p20 = fast_exp2(y0), p21 = fast_exp2(y1);
+          if (masked) {
+            if (kbase + c > lim) p10 = p20 = 0.f;
+            if (kbase + c + 1 > lim) p11 = p21 = 0.f;
+          }
+          if (kWindow && wedge) {
+            if (kbase + c < lo && !(kSink && kbase + c < p.sink)) p10 = p20 = 0.f;
+            if (kbase + c + 1 < lo && !(kSink && kbase + c + 1 < p.sink)) p11 = p21 = 0.f;
+          }
+          const uint64_t dpp = f2_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
+          const uint64_t d1 = f2_mul(f2_pack(p10, p11), f2_add(dpp, ne1));
+          const uint64_t d2 = f2_mul(f2_mul(nlam, f2_pack(p20, p21)), f2_add(dpp, ne2));
+          float u0, u1;
+          f2_unpack(d1, u0, u1);
+          d1_pk[c >> 1] = pack_bf16x2(u0, u1);
+          if (kFineBlock) d1_lo[c >> 1] = pack_rest(u0, u1, d1_pk[c >> 1]);
+          f2_unpack(d2, u0, u1);
+          d2_pk[c >> 1] = pack_bf16x2(u0, u1);
+          if (kFineBlock) d2_lo[c >> 1] = pack_rest(u0, u1, d2_pk[c >> 1]);
         }
-        if (kWindow && wedge) {
-          if (kbase + c < lo && !(kSink && kbase + c < p.sink)) p10 = p20 = 0.f;
-          if (kbase + c + 1 < lo && !(kSink && kbase + c + 1 < p.sink)) p11 = p21 = 0.f;
+        st_packed(trow + kTmS1 + col0, d1_pk);
+        st_packed(trow + kTmS2 + col0, d2_pk);
+        if constexpr (kFineBlock) {
+          st_packed(trow + kTmS1 + col0 + kCols / 2, d1_lo);
+          st_packed(trow + kTmS2 + col0 + kCols / 2, d2_lo);
         }
-        const uint64_t dpp = f2_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
-        const uint64_t d1 = f2_mul(f2_pack(p10, p11), f2_add(dpp, ne1));
-        const uint64_t d2 = f2_mul(f2_mul(nlam, f2_pack(p20, p21)), f2_add(dpp, ne2));
-        float u0, u1;
-        f2_unpack(d1, u0, u1);
-        d1_pk[c >> 1] = pack_bf16x2(u0, u1);
-        f2_unpack(d2, u0, u1);
-        d2_pk[c >> 1] = pack_bf16x2(u0, u1);
+      };
+      if constexpr (kSink) {
+        if (holds_sinks(t)) elementwise(std::true_type{});  // uniform over the CTA
+        else elementwise(std::false_type{});
+      } else {
+        elementwise(std::false_type{});
       }
-      st_packed(trow + kTmS1 + col0, d1_pk);
-      st_packed(trow + kTmS2 + col0, d2_pk);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(kPReady + cg / kGroupsPerChain));
@@ -1205,6 +1245,7 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   Params p;
   cudaError_t e;
   SinkPlan plan = {};
+  p.fine_keys = sink < kFineKeys ? sink : kFineKeys;
   if (o_branch_f32) {
     // the sink form; window <= 0: every earlier key, the causal mask
     if (window <= 0) {

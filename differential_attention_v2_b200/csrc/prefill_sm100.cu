@@ -136,6 +136,7 @@ struct Params {
   int B, S, Hq, Hkv, causal;
   int window;             // causal sliding window (keys i-window+1 .. i); 0 = none
   int sink;               // with a window: keys 0 .. sink-1 stay visible (kSink instances)
+  int fine_keys;          // kFine: P of KV tiles that start below this key is two bf16 terms
   const int* cu_seqlens;  // packed sequences: sequence b is tokens cu[b] .. cu[b+1]-1; null = [B,S]
   int n_row_tiles;
   int n_items;            // B * (Hq/2) * n_row_tiles
@@ -354,6 +355,36 @@ __device__ __forceinline__ float exp_pack_store(const uint32_t (&sr)[4][32], int
   return (s0 + s1) + (s2 + s3);
 }
 
+// The same as two bf16 terms: the second at columns 64 + 32*half on. 16 keys at a time: the two terms
+// of more would not fit the registers beside the row's scores.
+__device__ __forceinline__ float exp_pack_store_fine(const uint32_t (&sr)[4][32], int half, float scale, float m_use,
+                                                     uint32_t taddr) {
+  const uint64_t scale2 = f2_pack(scale, scale);
+  const uint64_t negm2 = f2_pack(-m_use, -m_use);
+  uint64_t sum = f2_pack(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t pk[8], rest[8];
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const uint32_t* x = sr[2 * half + (q >> 1)] + 16 * (q & 1) + e;
+      const uint64_t arg = f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), scale2, negm2);
+      float a0, a1;
+      f2_unpack(arg, a0, a1);
+      const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+      sum = f2_add(sum, f2_pack(p0, p1));
+      const uint32_t hi = pack_bf16x2(p0, p1);
+      pk[e >> 1] = hi;
+      rest[e >> 1] = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+    }
+    tmem_st_32x32b_x8(taddr + 32 * half + 8 * q, pk);
+    tmem_st_32x32b_x8(taddr + 64 + 32 * half + 8 * q, rest);
+  }
+  float s0, s1;
+  f2_unpack(sum, s0, s1);
+  return s0 + s1;
+}
+
 // 16 bytes of a stream read once (not kept in L1).
 __device__ __forceinline__ uint4 ld_stream_v4(const void* ptr) {
   uint4 v;
@@ -444,7 +475,10 @@ __device__ __forceinline__ void arrive_for_mma(uint32_t bar, int lane) {
 //   * a wait that gives up raises the abort flag of both CTAs; both CTAs leave through one
 //     cluster barrier, after every copy and commit addressed to them has landed.
 // kSink (with kWindow, one CTA per item): the first p.sink keys stay visible below the window.
-template <bool kVarlen, bool kWindow, bool kPair, bool kLamFused = false, bool kSink = false>
+// kFine (with kSink, training): P of the tiles that hold sinks enters P V as two bf16 terms, over S's
+// other 64 columns. The sinks' weights are most of a row's, and O_b's error through their rounding is
+// the backward's E = dO . O_b off by the same amount for all of the row's keys.
+template <bool kVarlen, bool kWindow, bool kPair, bool kLamFused = false, bool kSink = false, bool kFine = false>
 __global__ void __launch_bounds__(kThreads, 1)
 diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKh,
@@ -663,7 +697,8 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         // O_b (+)= P_b V for this CTA's KV tile number n (ring stage n % kStages, P barrier
         // phase n & 1): the first 64 keys as soon as that half of P is in TMEM, the other 64
         // when the second half is. acc = false starts the item's sum.
-        auto issue_pv = [&](uint32_t o_tmem, uint32_t p_tmem, int n, bool acc, uint32_t half0, uint32_t half1) {
+        auto issue_pv = [&](uint32_t o_tmem, uint32_t p_tmem, int n, bool acc, uint32_t half0, uint32_t half1,
+                            bool fine) {
   #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (!pwait_x<kPair>(h ? half1 : half0, n & 1, abort_flag, flag_addr)) return false;
@@ -674,9 +709,17 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
               if constexpr (kPair) mma_bf16_ts_pair(o_tmem, p_tmem + kk * 8, desc_v(n % kStages, kk), idesc_pv, acc_kk);
               else mma_bf16_ts(o_tmem, p_tmem + kk * 8, desc_v(n % kStages, kk), idesc_pv, acc_kk);
             }
+            if (kFine && fine) {
+              // (not unrolled: this warp's 96 registers hold no more descriptors, and a spill in
+              // the issue loop costs every tile)
+  #pragma unroll 1
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                mma_bf16_ts(o_tmem, p_tmem + 64 + kk * 8, desc_v(n % kStages, kk), idesc_pv, 1u);
+            }
           }
           return true;
         };
+        auto fine_tile = [&](int j) -> bool { return kFine && kv_tile<kSink>(w, j) * BN < p.fine_keys; };
         int n0 = 0;       // KV tiles of earlier items
         int n_items = 0;  // items done
         // the four 128-column accumulators fill the 512 allocated columns from column 0
@@ -696,7 +739,8 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
               mma_ss(tmem + kTmS1, desc_q(0, kk), desc_k(s, kk), idesc_qk, kk > 0 ? 1u : 0u);
             commit(kSFull + 0);
             if (j > 0) {
-              if (!(ok = issue_pv(tmem + kTmO2, tmem + kTmS2, n - 1, j > 1, bar(kPFull + 2), bar(kPFull + 3)))) break;
+              if (!(ok = issue_pv(tmem + kTmO2, tmem + kTmS2, n - 1, j > 1, bar(kPFull + 2), bar(kPFull + 3),
+                                   fine_tile(j - 1)))) break;
               commit(kVEmpty + (n - 1) % kStages);
             }
   #pragma unroll
@@ -712,11 +756,12 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
               if (!(ok = pwait_x<kPair>(bar(kOEmpty), (n_items - 1) & 1, abort_flag, flag_addr))) break;
               tc_fence_after();
             }
-            if (!(ok = issue_pv(tmem + kTmO1, tmem + kTmS1, n, j > 0, bar(kPFull + 0), bar(kPFull + 1)))) break;
+            if (!(ok = issue_pv(tmem + kTmO1, tmem + kTmS1, n, j > 0, bar(kPFull + 0), bar(kPFull + 1), fine_tile(j)))) break;
           }
           if (!ok) break;
           const int nl = n0 + w.n_kv - 1;
-          if (!(ok = issue_pv(tmem + kTmO2, tmem + kTmS2, nl, w.n_kv > 1, bar(kPFull + 2), bar(kPFull + 3)))) break;
+          if (!(ok = issue_pv(tmem + kTmO2, tmem + kTmS2, nl, w.n_kv > 1, bar(kPFull + 2), bar(kPFull + 3),
+                               fine_tile(w.n_kv - 1)))) break;
           commit(kVEmpty + nl % kStages);
           commit(kOFull);
           n0 += w.n_kv;
@@ -883,6 +928,17 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
         const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
         float lsum = 0.f;
+        if constexpr (kFine) {
+          if (j * BN < p.fine_keys) {  // uniform over the CTA
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              l_run += exp_pack_store_fine(sr, half, p.scale_log2, m_use, trow + s_col);
+              tmem_st_wait();
+              arrive_for_mma<kPair>(bar(kPFull + 2 * br + half), lane);
+            }
+            continue;
+          }
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           // a half no row of the warp sees gets P = 0 without its exponentials (all 2^-inf =
@@ -976,8 +1032,8 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
               store_row32(p.o_branch + ((w.row_base + qi) * p.Hq + 2 * w.pair + hb) * HD + col, ob);
             }
           }
-          if constexpr (kSink) {
-            if (p.o_branch_f32 != nullptr && row_valid) {
+          if constexpr (kFine) {
+            if (row_valid) {
 #pragma unroll
               for (int hb = 0; hb < 2; ++hb) {
                 const uint32_t* o = hb ? o2 : o1;
@@ -1058,6 +1114,7 @@ cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   using namespace prefill;
   Params p;
   p.sink = window > 0 ? sink : 0;
+  p.fine_keys = sink < kFineKeys ? sink : kFineKeys;
   p.o_branch_f32 = o_branch_f32;
   p.lambda = lambda;
   p.out = out;
@@ -1132,8 +1189,12 @@ cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
                                          : diffattn_prefill_sm100<false, false, false>);
   // (a training forward that wants fp32 O_b takes the sink form whatever its window)
   if (p.sink > 0 || o_branch_f32 != nullptr) {
-    kernel = cu_seqlens ? diffattn_prefill_sm100<true, true, false, false, true>
-                        : diffattn_prefill_sm100<false, true, false, false, true>;
+    if (o_branch_f32 != nullptr)
+      kernel = cu_seqlens ? diffattn_prefill_sm100<true, true, false, false, true, true>
+                          : diffattn_prefill_sm100<false, true, false, false, true, true>;
+    else
+      kernel = cu_seqlens ? diffattn_prefill_sm100<true, true, false, false, true>
+                          : diffattn_prefill_sm100<false, true, false, false, true>;
     if (window <= 0) p.window = S;  // every earlier key: the causal mask
   }
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);

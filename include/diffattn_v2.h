@@ -480,7 +480,9 @@ DA2_API int diffattn_v2_prefill_varlen_window_sink(const void* q, const void* k,
  * Training pass of the window with sinks. The forward's outputs and the backward's gradients are
  * those of diffattn_v2_prefill_window_train / diffattn_v2_backward_window (and the packed forms),
  * but o_branch is FP32 [B,S,Hq,D] ([T,Hq,D]): sinks draw most of a row's weight to one key, where
- * dS = A (dO.v_j - dO.O_b) is a small difference of large terms that a bf16 O_b would drown. A
+ * dS = A (dO.v_j - dO.O_b) is a small difference of large terms that a bf16 O_b would drown. For the
+ * same reason the products over (the first 512) sink keys keep their weights and dS as two bf16 terms,
+ * so that `out` here is nearer the exact value than the inference call's, not bit for bit the same. A
  * query that sees a single key has a constant softmax: its dq, and its part of dk, are exactly 0.
  * The workspace needs no initialisation; calls that share one must not overlap on the GPU. The
  * result is deterministic (no atomics).

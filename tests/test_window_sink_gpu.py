@@ -125,7 +125,7 @@ def test_training_pass_matches_oracle(da, B, S, Hq, Hkv, window, sink):
     grads = da.backward(*x, ob, lse, d["dout"], window=window, sink=sink)
     _ok(da)
     assert ob.dtype == torch.float32
-    assert torch.equal(out, da.prefill_window(*x, window, sink=sink))
+    bf16_close(out, ora.prefill(inp["q"], inp["k"], inp["v"], inp["lam"], window=window, sink=sink), "train out")
     ref = ora.prefill_backward(inp["q"], inp["k"], inp["v"], inp["lam"], inp["dout"], window=window, sink=sink)
     _grads_close(grads, ref, f"S={S} W={window} s={sink}")
     assert torch.count_nonzero(grads[0][:, 0]).item() == 0  # query 0 sees one key
@@ -139,9 +139,32 @@ def test_packed_training_pass_matches_oracle(da, lens, Hq, Hkv, window, sink):
     out, ob, lse = da.prefill_varlen_train(*x, *tail, window=window, sink=sink)
     grads = da.backward_varlen(*x, ob, lse, d["dout"], *tail, window=window, sink=sink)
     _ok(da)
-    assert torch.equal(out, da.prefill_varlen_window(*x, *tail, window, sink=sink))
+    bf16_close(out, ora.prefill_varlen(inp["q"], inp["k"], inp["v"], inp["lam"], cu, window=window, sink=sink), "train out")
     ref = ora.prefill_backward_varlen(inp["q"], inp["k"], inp["v"], inp["lam"], inp["dout"], cu, window=window, sink=sink)
     _grads_close(grads, ref, f"packed {lens}")
+
+
+def test_dq_where_many_alike_sinks_share_the_weight(da):
+    """Sinks that resemble one another: the roundings of their dS add up in dQ along the common direction
+    unless they are kept apart. Relative to dQ its own rounding is at most half a bf16 step, 2^-8; a
+    common-mode error of dS products rounded at 2^-8 each would be of that size again."""
+    S, sink, window = 500, 64, 60
+    g = torch.Generator().manual_seed(6)
+    u = torch.randn(128, generator=g)
+    u /= u.norm()
+    inp = _case(1, S, 4, 1, seed=78)
+    inp["q"] = (inp["q"].float() + 2 * u).bfloat16()
+    inp["k"][:, :sink] = (inp["k"][:, :sink].float() + 18 * u).bfloat16()
+    d = {k: v.cuda() for k, v in inp.items()}
+    x = (d["q"], d["k"], d["v"], d["lam"])
+    for w, s in ((window, sink), (S, sink), (window, S)):  # and where the mask is the plain causal one
+        out, ob, lse = da.prefill_train(*x, window=w, sink=s)
+        grads = da.backward(*x, ob, lse, d["dout"], window=w, sink=s)
+        _ok(da)
+        ref = ora.prefill_backward(inp["q"], inp["k"], inp["v"], inp["lam"], inp["dout"], window=w, sink=s)
+        _grads_close(grads, ref, f"alike sinks W={w} s={s}")
+        off = np.linalg.norm(to64(grads[0]) - ref[0]) / np.linalg.norm(ref[0])
+        assert off <= 2.0 ** -8, off
 
 
 def test_gradients_where_one_sink_takes_nearly_all_weight(da):
