@@ -6,6 +6,7 @@ The binding is loaded on first use of any of its names; if the library is missin
 use raises ImportError (there is no fallback implementation).
 """
 import importlib
+import inspect
 
 _BINDING_NAMES = (
     "prefill", "prefill_window", "prefill_varlen", "prefill_varlen_window", "prefill_f32", "prefill_train", "backward",
@@ -20,5 +21,8 @@ __all__ = list(_BINDING_NAMES)
 def __getattr__(name):
     if name in _BINDING_NAMES:
         mod = importlib.import_module("._lib", __name__)
-        return getattr(mod, name)
+        value = getattr(mod, name)
+        if inspect.isfunction(value):
+            globals()[name] = value  # found without this detour (1 us) from the second use on
+        return value
     raise AttributeError(name)

@@ -347,6 +347,13 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// The two halves of a cluster barrier: arrive without ordering memory, wait for all (not the
+// .aligned forms, as below).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // Every thread of both CTAs: memory operations before it are visible to both CTAs after it.
 // (Not the .aligned form: a warp may reach it from diverged paths.)
 __device__ __forceinline__ void cluster_sync() {
