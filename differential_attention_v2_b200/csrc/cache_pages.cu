@@ -168,9 +168,10 @@ __device__ __forceinline__ int release(int32_t* refs, int num_pages, int e) {
 __device__ __forceinline__ int pages_of(int len, int shift) { return (max(len, 0) + (1 << shift) - 1) >> shift; }
 
 // ---------------------------------------------------------------------------------- extend
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
 extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_new, int32_t* result, int B,
               int max_pages, int shift, int num_pages) {
+  pdl_wait();
   __shared__ Shared sh;
   __shared__ int pre[kMaxCacheSeqs], first[kMaxCacheSeqs];
   cg::cluster_group cl = cg::this_cluster();
@@ -210,9 +211,10 @@ extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_
 }
 
 // ------------------------------------------------------------------------------------ fork
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
 fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* parents, const int32_t* children,
             int2* copies, int32_t* result, int n, int B, int max_pages, int shift, int num_pages) {
+  pdl_wait();
   __shared__ Shared sh;
   __shared__ int pre[kMaxCacheSeqs], kid[kMaxCacheSeqs], len[kMaxCacheSeqs];
   cg::cluster_group cl = cg::this_cluster();
@@ -287,9 +289,10 @@ fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* pare
 }
 
 // ------------------------------------------------------------------------------------ trim
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
 trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B, int max_pages, int shift,
             int num_pages, int window, int keep) {
+  pdl_wait();
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31;
@@ -319,9 +322,10 @@ trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* resu
 }
 
 // ------------------------------------------------------------------------------------ free
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
 free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result, int n, int B,
             int max_pages, int num_pages) {
+  pdl_wait();
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31;
@@ -354,9 +358,10 @@ free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs
 
 // --------------------------------------------------------------------------------- compact
 // n live pages; the r-th live page at or behind n goes to the r-th free one before it.
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
 compact_kernel(const int32_t* table, const int32_t* refs, int32_t* table_out, int32_t* refs_out, int2* moves,
                int32_t* result, int B, int max_pages, int num_pages) {
+  pdl_wait();
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31;
@@ -427,15 +432,16 @@ constexpr int kCopyUnroll = 4;
 constexpr int kPieceVecs = kCopyThreads * kCopyUnroll;
 
 __global__ void __launch_bounds__(kCopyThreads)
-copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const int2* __restrict__ copies, int n, int num_pages,
+copy_kernel(uint4* k, uint4* v, const int2* copies, int n, int num_pages,
             int page_vecs, int pieces) {
+  pdl_wait();
   const long long items = static_cast<long long>(n) * 2 * pieces;
   long long it = blockIdx.x;
   if (it >= items) return;
-  int2 next = __ldg(copies + it / pieces / 2);
+  int2 next = *(copies + it / pieces / 2);
   for (; it < items; it += gridDim.x) {
     const int2 c = next;
-    if (it + gridDim.x < items) next = __ldg(copies + (it + gridDim.x) / pieces / 2);  // while this piece is copied
+    if (it + gridDim.x < items) next = *(copies + (it + gridDim.x) / pieces / 2);  // while this piece is copied
     if (c.x < 0 || c.y < 0 || c.x >= num_pages || c.y >= num_pages) continue;
     uint4* pool = (it / pieces) & 1 ? v : k;
     const uint4* src = pool + static_cast<size_t>(c.x) * page_vecs;
@@ -456,43 +462,38 @@ copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const int2* __restrict
 cudaError_t launch_cache_extend(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_new,
                                 int32_t* result, int B, int max_pages, int page_shift, int num_pages,
                                 cudaStream_t stream) {
-  pages::extend_kernel<<<pages::kCtas, pages::kThreads, 0, stream>>>(table, seqlens, refs, n_new, result, B, max_pages,
-                                                                     page_shift, num_pages);
-  return cudaGetLastError();
+  return launch_chained(pages::extend_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
+                        table, seqlens, refs, n_new, result, B, max_pages, page_shift, num_pages);
 }
 
 cudaError_t launch_cache_fork(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* parents,
                               const int32_t* children, int32_t* copies, int32_t* result, int n, int B, int max_pages,
                               int page_shift, int num_pages, cudaStream_t stream) {
-  pages::fork_kernel<<<pages::kCtas, pages::kThreads, 0, stream>>>(table, seqlens, refs, parents, children,
-                                                                   reinterpret_cast<int2*>(copies), result, n, B,
-                                                                   max_pages, page_shift, num_pages);
-  return cudaGetLastError();
+  return launch_chained(pages::fork_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
+                        table, seqlens, refs, parents, children, reinterpret_cast<int2*>(copies), result, n, B,
+                        max_pages, page_shift, num_pages);
 }
 
 cudaError_t launch_cache_trim(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B,
                               int max_pages, int page_shift, int num_pages, int window, int sink,
                               cudaStream_t stream) {
   const int keep = static_cast<int>((static_cast<long long>(sink) + (1 << page_shift) - 1) >> page_shift);
-  pages::trim_kernel<<<pages::kCtas, pages::kThreads, 0, stream>>>(table, seqlens, refs, result, B, max_pages,
-                                                                   page_shift, num_pages, window, keep);
-  return cudaGetLastError();
+  return launch_chained(pages::trim_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
+                        table, seqlens, refs, result, B, max_pages, page_shift, num_pages, window, keep);
 }
 
 cudaError_t launch_cache_free(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result,
                               int n, int B, int max_pages, int num_pages, cudaStream_t stream) {
-  pages::free_kernel<<<pages::kCtas, pages::kThreads, 0, stream>>>(table, seqlens, refs, seqs, result, n, B, max_pages,
-                                                                   num_pages);
-  return cudaGetLastError();
+  return launch_chained(pages::free_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
+                        table, seqlens, refs, seqs, result, n, B, max_pages, num_pages);
 }
 
 cudaError_t launch_cache_compact(const int32_t* table, const int32_t* refs, int32_t* table_out, int32_t* refs_out,
                                  int32_t* moves, int32_t* result, int B, int max_pages, int num_pages,
                                  cudaStream_t stream) {
-  pages::compact_kernel<<<pages::kCtas, pages::kThreads, 0, stream>>>(table, refs, table_out, refs_out,
-                                                                      reinterpret_cast<int2*>(moves), result, B,
-                                                                      max_pages, num_pages);
-  return cudaGetLastError();
+  return launch_chained(pages::compact_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
+                        table, refs, table_out, refs_out, reinterpret_cast<int2*>(moves), result, B, max_pages,
+                        num_pages);
 }
 
 cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int n, int num_pages, size_t page_bytes,
@@ -508,10 +509,9 @@ cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int
   // Many short-lived CTAs: 994 pages of 128 KB in both caches took 80 us (521 MB, 6.5 TB/s) with 64 CTAs
   // for every SM, 95 with the 8 that are resident at a time.
   const long long most = 64LL * n_sms;
-  pages::copy_kernel<<<static_cast<unsigned>(items < most ? items : most), pages::kCopyThreads, 0, stream>>>(
-      static_cast<uint4*>(k), static_cast<uint4*>(v), reinterpret_cast<const int2*>(copies), n, num_pages, page_vecs,
-      pieces);
-  return cudaGetLastError();
+  return launch_chained(pages::copy_kernel, dim3(static_cast<unsigned>(items < most ? items : most)),
+                        dim3(pages::kCopyThreads), 0, 0, stream, static_cast<uint4*>(k), static_cast<uint4*>(v),
+                        reinterpret_cast<const int2*>(copies), n, num_pages, page_vecs, pieces);
 }
 
 }  // namespace da2

@@ -85,6 +85,7 @@ template <int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   static_assert(sizeof(Merge<NT>) <= kOffBar, "merge buffers");
+  pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -115,10 +116,10 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   const int n_pairs = p.Hq >> 1;
   const size_t pair0 = static_cast<size_t>(b) * n_pairs + g * (group / 2);
   const int my_pair = rank + ctas * warp;
-  const float lam0 = my_pair < group / 2 ? __ldg(p.lambda + pair0 + my_pair) : 0.f;
+  const float lam0 = my_pair < group / 2 ? *(p.lambda + pair0 + my_pair) : 0.f;
 
   // visible keys: [0, ns) and [lo, n); chunks 0 .. n_head-1 and from first_w on
-  const int n = min(max(__ldg(p.seqlens + b), 0), p.Smax);
+  const int n = min(max(*(p.seqlens + b), 0), p.Smax);
   const int lo = max(0, n - p.window);
   const int ns = min(p.sink, lo);
   const int first_w = lo / kTok;
@@ -148,8 +149,8 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     if (k >= mine) return;
     const int t = chunk_tok(k), lp = t >> p.page_shift;
     const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
-    if (checked(lp < p.max_pages, p.err)) entry0 = __ldg(row + lp);
-    if (small_pages && t + 8 < n) entry1 = __ldg(row + lp + 1);
+    if (checked(lp < p.max_pages, p.err)) entry0 = *(row + lp);
+    if (small_pages && t + 8 < n) entry1 = *(row + lp + 1);
   };
   // chunk k into its slot (the whole warp calls; lane 0 copies)
   auto issue = [&](int k) {
@@ -196,8 +197,8 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
         p.q + (static_cast<size_t>(b) * p.Hq + g * group + (hv ? h : 0)) * HD);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-      qf[nt][kk][0] = hv ? __ldg(qrow + 8 * kk + tq) : 0u;
-      qf[nt][kk][1] = hv ? __ldg(qrow + 8 * kk + tq + 4) : 0u;
+      qf[nt][kk][0] = hv ? *(qrow + 8 * kk + tq) : 0u;
+      qf[nt][kk][1] = hv ? *(qrow + 8 * kk + tq + 4) : 0u;
     }
     m_run[nt][0] = m_run[nt][1] = -INFINITY;
     l_part[nt][0] = l_part[nt][1] = 0.f;
@@ -397,7 +398,7 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
       res[br][3] = __fmul_rn(acc.w, inv);
     }
     const size_t row = pair0 + i;
-    const float lam = i == my_pair ? lam0 : __ldg(p.lambda + row);
+    const float lam = i == my_pair ? lam0 : *(p.lambda + row);
     uint2 packed;
     packed.x = pack_bf16x2(__fmaf_rn(-lam, res[1][0], res[0][0]), __fmaf_rn(-lam, res[1][1], res[0][1]));
     packed.y = pack_bf16x2(__fmaf_rn(-lam, res[1][2], res[0][2]), __fmaf_rn(-lam, res[1][3], res[0][3]));
@@ -453,21 +454,8 @@ cudaError_t launch_decode_sink(const CUtensorMap& tmK, const CUtensorMap& tmV, c
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(c), static_cast<unsigned>(Hkv), static_cast<unsigned>(B));
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, tmK, tmV, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_chained(kernel, dim3(static_cast<unsigned>(c), static_cast<unsigned>(Hkv), static_cast<unsigned>(B)),
+                        dim3(kThreads), smem, c, stream, tmK, tmV, p);
 }
 
 }  // namespace da2

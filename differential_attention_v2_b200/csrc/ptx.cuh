@@ -35,6 +35,12 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   return t;
 }
 
+// Programmatic dependent launch: waits until the kernels before this one in the stream are complete and
+// their writes visible. First statement of a kernel that launch_chained starts, whose CTAs may be
+// placed earlier than that. Such a kernel reads nothing through the read-only path (__ldg, const
+// __restrict__), whose loads a compiler may move ahead of the wait.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

@@ -80,16 +80,16 @@ __device__ __forceinline__ long long cache_row(const RopeParams& p, int t, int l
     b = -1;
     for (int b0 = 0; b0 < p.B && b < 0; b0 += 32) {
       const int i = b0 + lane;
-      const bool in = i < p.B && __ldg(p.cu_seqlens + i) <= t && t < __ldg(p.cu_seqlens + i + 1);
+      const bool in = i < p.B && *(p.cu_seqlens + i) <= t && t < *(p.cu_seqlens + i + 1);
       const unsigned m = __ballot_sync(0xffffffffu, in);
       if (m) b = b0 + __ffs(m) - 1;
     }
     if (b < 0) return -2;  // behind the last sequence
-    end = __ldg(p.cu_seqlens + b + 1);
+    end = *(p.cu_seqlens + b + 1);
   }
-  const int at = __ldg(p.seqlens + b) - (end - t);
+  const int at = *(p.seqlens + b) - (end - t);
   if (at < 0 || (at >> p.page_shift) >= p.max_pages) return -1;
-  const int page = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + (at >> p.page_shift));
+  const int page = *(p.block_table + static_cast<size_t>(b) * p.max_pages + (at >> p.page_shift));
   if (page < 0 || page >= p.num_pages) return -1;
   return (static_cast<long long>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
 }
@@ -131,6 +131,7 @@ __device__ __forceinline__ void walk(const T* src, T* dst, int h, int step, int 
 template <typename T, int N, bool kInter, bool kAppend>
 __global__ void __launch_bounds__(kThreads, kAppend ? 8 : 10)
 rope_kernel(const RopeParams p, const int chunks, const int chunk_heads) {
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int t = static_cast<int>(item / chunks);
@@ -167,8 +168,8 @@ rope_kernel(const RopeParams p, const int chunks, const int chunk_heads) {
       if (rot && e0 < N) {
         int axis = 0;
         while (axis + 1 < p.n_axes && c >= p.sec_end[axis]) ++axis;
-        double turn = static_cast<double>(__ldg(p.positions + static_cast<size_t>(axis) * p.T + t)) *
-                      static_cast<double>(__ldg(p.inv_freq + c)) * 0.15915494309189535;
+        double turn = static_cast<double>(*(p.positions + static_cast<size_t>(axis) * p.T + t)) *
+                      static_cast<double>(*(p.inv_freq + c)) * 0.15915494309189535;
         turn -= rint(turn);
         sincospif(static_cast<float>(2.0 * turn), &s, &k);
         if (p.inverse) s = -s;
@@ -224,8 +225,8 @@ cudaError_t launch_n(const RopeParams& p, cudaStream_t stream) {
   auto kernel = append ? (p.interleaved ? rope_kernel<T, N, true, true> : rope_kernel<T, N, false, true>)
                        : (p.interleaved ? rope_kernel<T, N, true, false> : rope_kernel<T, N, false, false>);
   const long long items = static_cast<long long>(p.T) * chunks;
-  kernel<<<static_cast<unsigned>((items + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p, chunks, chunk_heads);
-  return cudaGetLastError();
+  return launch_chained(kernel, dim3(static_cast<unsigned>((items + kWarps - 1) / kWarps)), dim3(kThreads), 0, 0, stream,
+                        p, chunks, chunk_heads);
 }
 
 // The widest vectors (16 bytes at most) that every pointer, stride and section border allows.
