@@ -33,11 +33,10 @@ constexpr int kAllWarps = kCtas * kWarps;
 constexpr int kAllThreads = kCtas * kThreads;
 
 struct Shared {
-  int warp_cnt[kWarps];  // pages counted by each warp of this CTA
-  int cta_cnt;           // their sum
-  int flag;              // this CTA found a reason to refuse
-  int extra;
-  int scan[kWarps + 1];
+  int cnt[kWarps];      // of each warp of this CTA
+  int flag;             // this CTA found a reason to refuse
+  int scan[kWarps];
+  int2 in[2][kCtas];    // what each CTA of the cluster sent: (sum, flag), by exchange
 };
 
 // Pages [lo, hi) of warp `w` of the cluster: consecutive, a multiple of 32 long.
@@ -57,56 +56,44 @@ __device__ __forceinline__ int count_pages(const int32_t* refs, int lo, int hi, 
   return n;
 }
 
-// Exclusive prefix over the cluster's warps of one count per warp, and the total. Ends with the
-// counts of every CTA read (the caller still has to meet the cluster before it exits).
-__device__ __forceinline__ int cluster_prefix(Shared& sh, int mine, int& total) {
+// One value per warp and one flag per CTA, for all of the cluster: returns the sum of the warps before
+// this one, the total and whether any flag is set. Every CTA stores its sum and flag into the shared
+// memory of all eight, so that one barrier is enough: nothing is read from another CTA after it, and no
+// CTA needs to wait for others before it exits. (Leaving them to be read took a barrier before and one
+// after, and a trip between SMs in between.) The barrier also orders all that any CTA read before it
+// ahead of all that is written after it. `slot`: 0 or 1, another for each exchange of a kernel. The
+// first exchange follows cluster_arrive_relaxed at the kernel's start.
+__device__ __forceinline__ int exchange(Shared& sh, int slot, int mine, int& total, bool& flag) {
   cg::cluster_group cl = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) sh.warp_cnt[warp] = mine;
+  if (lane == 0) sh.cnt[warp] = mine;
   __syncthreads();
   int base = 0, sum = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += sh.warp_cnt[w];
-    sum += sh.warp_cnt[w];
+    if (w < warp) base += sh.cnt[w];
+    sum += sh.cnt[w];
   }
-  if (threadIdx.x == 0) sh.cta_cnt = sum;
+  const int rank = static_cast<int>(cl.block_rank());
+  if (slot == 0) cluster_wait();  // every CTA is running
+  if (threadIdx.x < kCtas) *cl.map_shared_rank(&sh.in[slot][rank], threadIdx.x) = make_int2(sum, sh.flag);
   cl.sync();
   total = 0;
-  const int rank = static_cast<int>(cl.block_rank());
+  flag = false;
 #pragma unroll
   for (int r = 0; r < kCtas; ++r) {
-    const int c = *cl.map_shared_rank(&sh.cta_cnt, r);
-    if (r < rank) base += c;
-    total += c;
+    const int2 v = sh.in[slot][r];
+    if (r < rank) base += v.x;
+    total += v.x;
+    flag |= v.y != 0;
   }
   return base;
 }
 
-// Whether any CTA of the cluster raised its flag; orders everything read before it by any CTA
-// ahead of everything written after it.
-__device__ __forceinline__ bool cluster_any(Shared& sh) {
-  cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
-  int any = 0;
-#pragma unroll
-  for (int r = 0; r < kCtas; ++r) any |= *cl.map_shared_rank(&sh.flag, r);
-  return any != 0;
-}
-
-// Sum over the cluster of one value per thread; the value is for rank 0's thread 0.
-__device__ __forceinline__ int cluster_sum(Shared& sh, int v) {
-  cg::cluster_group cl = cg::this_cluster();
-  if (threadIdx.x == 0) sh.extra = 0;
-  __syncthreads();
+__device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0 && v != 0) atomicAdd(&sh.extra, v);
-  cl.sync();
-  int total = 0;
-  if (cl.block_rank() == 0 && threadIdx.x == 0)
-    for (int r = 0; r < kCtas; ++r) total += *cl.map_shared_rank(&sh.extra, r);
-  cl.sync();
-  return total;
+  return v;
 }
 
 // In-place inclusive prefix sum of a[0..n) in shared memory by the CTA.
@@ -172,6 +159,7 @@ __global__ void __launch_bounds__(kThreads)
 extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_new, int32_t* result, int B,
               int max_pages, int shift, int num_pages) {
   pdl_wait();
+  cluster_arrive_relaxed();
   __shared__ Shared sh;
   __shared__ int pre[kMaxCacheSeqs], first[kMaxCacheSeqs];
   cg::cluster_group cl = cg::this_cluster();
@@ -193,9 +181,10 @@ extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_
   block_scan(sh, pre, B);
   const int want = pre[B - 1];
   int lo, hi, total;
+  bool bad;
   warp_range(num_pages, gw, lo, hi);
-  const int base = cluster_prefix(sh, count_pages(refs, lo, hi, false, lane), total);
-  const bool refuse = cluster_any(sh) || want > total;
+  const int base = exchange(sh, 0, count_pages(refs, lo, hi, false, lane), total, bad);
+  const bool refuse = bad || want > total;
   if (!refuse) {
     take_free(refs, lo, hi, base, want, lane, [&](int r, int p) {
       const int b = owner_of(pre, B, r);
@@ -207,7 +196,6 @@ extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_
       for (int b = threadIdx.x; b < B; b += kThreads) seqlens[b] = max(seqlens[b], 0) + max(n_new[b], 0);
   }
   if (cl.block_rank() == 0 && threadIdx.x == 0) result[0] = refuse ? -1 : want;
-  cl.sync();  // no CTA leaves while another reads its counts
 }
 
 // ------------------------------------------------------------------------------------ fork
@@ -215,6 +203,7 @@ __global__ void __launch_bounds__(kThreads)
 fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* parents, const int32_t* children,
             int2* copies, int32_t* result, int n, int B, int max_pages, int shift, int num_pages) {
   pdl_wait();
+  cluster_arrive_relaxed();
   __shared__ Shared sh;
   __shared__ int pre[kMaxCacheSeqs], kid[kMaxCacheSeqs], len[kMaxCacheSeqs];
   cg::cluster_group cl = cg::this_cluster();
@@ -246,9 +235,9 @@ fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* pare
   block_scan(sh, pre, n);
   const int want = pre[n - 1];
   int lo, hi, total;
+  bool bad;
   warp_range(num_pages, gw, lo, hi);
-  const int base = cluster_prefix(sh, count_pages(refs, lo, hi, false, lane), total);
-  const bool bad = cluster_any(sh);
+  const int base = exchange(sh, 0, count_pages(refs, lo, hi, false, lane), total, bad);
   const bool refuse = bad || want > total;
   if (!refuse) {
     // a page of its own for each partly filled last page
@@ -285,7 +274,6 @@ fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* pare
   for (int i = gt; i < n; i += kAllThreads)
     if (refuse || pre[i] == (i > 0 ? pre[i - 1] : 0)) copies[i] = make_int2(-1, -1);
   if (gt == 0) result[0] = bad ? -2 : (refuse ? -1 : want);
-  cl.sync();
 }
 
 // ------------------------------------------------------------------------------------ trim
@@ -293,7 +281,9 @@ __global__ void __launch_bounds__(kThreads)
 trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B, int max_pages, int shift,
             int num_pages, int window, int keep) {
   pdl_wait();
+  cluster_arrive_relaxed();
   __shared__ Shared sh;
+  if (threadIdx.x == 0) sh.flag = 0;
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31;
   const int gw = static_cast<int>(cl.block_rank()) * kWarps + (threadIdx.x >> 5);
@@ -317,7 +307,9 @@ trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* resu
       }
     }
   }
-  const int total = cluster_sum(sh, freed);
+  int total;
+  bool none;
+  exchange(sh, 0, warp_sum(freed), total, none);
   if (cl.block_rank() == 0 && threadIdx.x == 0) result[0] = total;
 }
 
@@ -326,16 +318,17 @@ __global__ void __launch_bounds__(kThreads)
 free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result, int n, int B,
             int max_pages, int num_pages) {
   pdl_wait();
+  cluster_arrive_relaxed();
   __shared__ Shared sh;
+  if (threadIdx.x == 0) sh.flag = 0;
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cl.block_rank());
   const int gw = rank * kWarps + (threadIdx.x >> 5), gt = rank * kThreads + threadIdx.x;
-  if (threadIdx.x == 0) sh.flag = 0;
-  __syncthreads();
-  for (int i = gt; i < n; i += kAllThreads)
-    if (seqs[i] >= B) sh.flag = 1;
-  const bool bad = cluster_any(sh);
+  // every CTA looks at the whole list, so that none has to ask another before it changes anything
+  int found = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) found |= seqs[i] >= B ? 1 : 0;
+  const bool bad = __syncthreads_or(found) != 0;
   int freed = 0;
   if (!bad) {
     const int per = (max_pages + 127) / 128;
@@ -352,7 +345,9 @@ free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs
       if (l0 == 0 && lane == 0) seqlens[b] = 0;
     }
   }
-  const int total = cluster_sum(sh, freed);
+  int total;
+  bool none;
+  exchange(sh, 0, warp_sum(freed), total, none);
   if (gt == 0) result[0] = bad ? -2 : total;
 }
 
@@ -362,21 +357,20 @@ __global__ void __launch_bounds__(kThreads)
 compact_kernel(const int32_t* table, const int32_t* refs, int32_t* table_out, int32_t* refs_out, int2* moves,
                int32_t* result, int B, int max_pages, int num_pages) {
   pdl_wait();
+  cluster_arrive_relaxed();
   __shared__ Shared sh;
+  if (threadIdx.x == 0) sh.flag = 0;
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cl.block_rank());
   const int gw = rank * kWarps + (threadIdx.x >> 5), gt = rank * kThreads + threadIdx.x;
   int lo, hi, n;
+  bool none;
   warp_range(num_pages, gw, lo, hi);
-  const int base = cluster_prefix(sh, count_pages(refs, lo, hi, true, lane), n);
+  const int base = exchange(sh, 0, count_pages(refs, lo, hi, true, lane), n, none);
   // live pages before n: those of this warp's range, summed over the cluster
   int before = 0;
-  {
-    const int c = lo < n ? count_pages(refs, lo, min(hi, n), true, lane) : 0;
-    cl.sync();  // every CTA has read the counts of the first prefix
-    cluster_prefix(sh, c, before);
-  }
+  exchange(sh, 1, lo < n ? count_pages(refs, lo, min(hi, n), true, lane) : 0, before, none);
   const int n_moves = n - before;
   int2* mv = moves;
   int r_live = base;
@@ -420,7 +414,6 @@ compact_kernel(const int32_t* table, const int32_t* refs, int32_t* table_out, in
     table_out[i] = e;
   }
   if (gt == 0) result[0] = n;
-  cl.sync();
 }
 
 // ------------------------------------------------------------------------------ copy pages
