@@ -154,75 +154,8 @@ def _need(t, name, dtype, ndim):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _expect(t, name, dtype, shape, device):
-    """A contiguous tensor of this dtype and shape on this device."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got one on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-
-
-def _shape(t, name, ndim):
-    """The device and sizes of a call's leading tensor."""
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    return t.device, t.shape
-
-
-def _new(given, name, dtype, shape, device, stream):
-    """The caller's output tensor, or a new one that its stream may use."""
-    if given is not None:
-        _expect(given, name, dtype, shape, device)
-        return given
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                        else torch.cuda.ExternalStream(int(stream), device=device))
-    return t
-
-
-def _call(name, device, stream, *args):
-    """An entry point on the tensors' device and the given or that device's current stream."""
-    index = device.index
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream, device)
-    if index == torch._C._cuda_getDevice():
-        st = getattr(LIB, name)(*args, s)
-    else:
-        with torch.cuda.device(index):
-            st = getattr(LIB, name)(*args, s)
-    if st != OK:
-        _check(st, name)
-
-
 def version() -> int:
     return LIB.diffattn_v2_version()
-
-
-def _attention_inputs(q, k, v, lam, device):
-    """Checks q [..., Hq, D], k and v [..., Hkv, D] and lam [..., Hq/2]; returns Hkv."""
-    *lead, Hq, D = q.shape
-    if k.dim() != q.dim():
-        raise ValueError(f"k: expected {q.dim()} dimensions, got shape {tuple(k.shape)}")
-    Hkv = k.shape[-2]
-    _expect(q, "q", torch.bfloat16, q.shape, device)
-    _expect(k, "k", torch.bfloat16, (*lead, Hkv, D), device)
-    _expect(v, "v", torch.bfloat16, (*lead, Hkv, D), device)
-    _expect(lam, "lam", torch.float32, (*lead, Hq // 2), device)
-    return Hkv
-
-
-def _sequences(cu_seqlens, device):
-    n = cu_seqlens.numel()
-    if n < 1:
-        raise ValueError("cu_seqlens: expected B + 1 entries")
-    _expect(cu_seqlens, "cu_seqlens", torch.int32, (n,), device)
-    return n - 1
 
 
 def _window_of_sink(window, causal):
@@ -361,40 +294,15 @@ def backward_workspace_size(B, S, Hq) -> int:
     return int(LIB.diffattn_v2_backward_workspace_size(B, S, Hq))
 
 
-def _gradient_tensors(q, k, v, lam, o_branch, lse, dout, dq, dk, dv, dlam, device, stream):
-    """The backward's inputs and its gradient tensors (the caller's or new ones), in C order."""
-    *lead, Hq, D = q.shape
-    _expect(o_branch, "o_branch", torch.float32, q.shape, device)
-    _expect(lse, "lse", torch.float32, (*lead, Hq), device)
-    _expect(dout, "dout", torch.bfloat16, (*lead, Hq // 2, D), device)
-    grads = [_new(g, "d" + n, t.dtype, t.shape, device, stream)
-             for g, n, t in ((dq, "q", q), (dk, "k", k), (dv, "v", v), (dlam, "lam", lam))]
-    return [q, k, v, lam, o_branch, lse, dout, *grads]
-
-
-def _workspace(given, need, device, stream):
-    if given is None:
-        return _new(None, "workspace", torch.uint8, (max(need, 16),), device, stream)
-    if given.device != device or not given.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
-    return given
-
-
 def backward(q, k, v, lam, o_branch, lse, dout, causal=True, dq=None, dk=None, dv=None, dlam=None,
              workspace=None, window=None, stream=None, sink=None):
     """Gradients of the bf16 prefill: returns (dq, dk, dv, dlam) with the layouts of q, k, v, lam.
     With `window` the gradients of the causal sliding-window prefill, with `sink` besides those
     of the window with sinks (o_branch fp32)."""
     if sink is not None:
-        window, sink = _window_of_sink(window, causal), int(sink)
-        device, (B, S, Hq, D) = _shape(q, "q", 4)
-        Hkv = _attention_inputs(q, k, v, lam, device)
-        ptrs = _gradient_tensors(q, k, v, lam, o_branch, lse, dout, dq, dk, dv, dlam, device, stream)
-        need = LIB.diffattn_v2_backward_window_sink_workspace_size(B, S, Hq, Hkv, window, sink)
-        workspace = _workspace(workspace, need, device, stream)
-        _call("diffattn_v2_backward_window_sink", device, stream, *(t.data_ptr() for t in ptrs), B, S, Hq, Hkv, D,
-              window, sink, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        return tuple(ptrs[7:])
+        return _invoke(_BACKWARD_SINK, LIB.addresses["diffattn_v2_backward_window_sink"], q, k, v, lam, o_branch, lse, dout,
+                       _window_of_sink(window, causal), sink, dq, dk, dv, dlam,
+                       LIB.addresses["diffattn_v2_backward_window_sink_workspace_size"], workspace, stream)
     for t, n, nd in ((q, "q", 4), (k, "k", 4), (v, "v", 4), (o_branch, "o_branch", 4), (dout, "dout", 4)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 3)
@@ -470,17 +378,10 @@ def backward_varlen(q, k, v, lam, o_branch, lse, dout, cu_seqlens, max_seqlen, c
     """Gradients of the packed-sequence prefill: returns (dq, dk, dv, dlam) in the packed layouts.
     With `window` the gradients of the causal sliding-window packed prefill."""
     if sink is not None:  # with a window: the first `sink` keys stay visible, o_branch fp32
-        window, sink = _window_of_sink(window, causal), int(sink)
-        device, (T, Hq, D) = _shape(q, "q", 3)
-        Hkv = _attention_inputs(q, k, v, lam, device)
-        B = _sequences(cu_seqlens, device)
-        ptrs = _gradient_tensors(q, k, v, lam, o_branch, lse, dout, None, None, None, None, device, stream)
-        need = LIB.diffattn_v2_backward_varlen_window_sink_workspace_size(B, int(max_seqlen), T, Hq, Hkv, window, sink)
-        workspace = _workspace(workspace, need, device, stream)
-        _call("diffattn_v2_backward_varlen_window_sink", device, stream, *(t.data_ptr() for t in ptrs),
-              cu_seqlens.data_ptr(), B, int(max_seqlen), T, Hq, Hkv, D, window, sink, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size())
-        return tuple(ptrs[7:])
+        return _invoke(_BACKWARD_VARLEN_SINK, LIB.addresses["diffattn_v2_backward_varlen_window_sink"], q, k, v, lam,
+                       cu_seqlens, max_seqlen, o_branch, lse, dout, _window_of_sink(window, causal), sink, None, None,
+                       None, None, LIB.addresses["diffattn_v2_backward_varlen_window_sink_workspace_size"], workspace,
+                       stream)
     for t, n, nd in ((q, "q", 3), (k, "k", 3), (v, "v", 3), (o_branch, "o_branch", 3), (dout, "dout", 3)):
         _need(t, n, torch.bfloat16, nd)
     _need(lam, "lam", torch.float32, 2)
@@ -807,6 +708,15 @@ _TRAIN_SINK = _entry("diffattn_v2_prefill_window_sink_train", _BATCH + """#windo
 _TRAIN_VARLEN_SINK = _entry("diffattn_v2_prefill_varlen_window_sink_train", _PACKED + """#window #sink
     >out:bf16[T,Hq/2,D] >o_branch:f32[T,Hq,D] >lse:f32[T,Hq]
     -> q k v lam out o_branch lse cu_seqlens B max_seqlen T Hq Hkv D window sink => out o_branch lse""")
+_BACKWARD_SINK = _entry("diffattn_v2_backward_window_sink", _BATCH + """o_branch:f32[B,S,Hq,D] lse:f32[B,S,Hq]
+    dout:bf16[B,S,Hq/2,D] #window #sink >dq:bf16[B,S,Hq,D] >dk:bf16[B,S,Hkv,D] >dv:bf16[B,S,Hkv,D] >dlam:f32[B,S,Hq/2]
+    @workspace(B,S,Hq,Hkv,window,sink)
+    -> q k v lam o_branch lse dout dq dk dv dlam B S Hq Hkv D window sink workspace workspace.n => dq dk dv dlam""")
+_BACKWARD_VARLEN_SINK = _entry("diffattn_v2_backward_varlen_window_sink", _PACKED + """o_branch:f32[T,Hq,D] lse:f32[T,Hq]
+    dout:bf16[T,Hq/2,D] #window #sink >dq:bf16[T,Hq,D] >dk:bf16[T,Hkv,D] >dv:bf16[T,Hkv,D] >dlam:f32[T,Hq/2]
+    @workspace(B,max_seqlen,T,Hq,Hkv,window,sink)
+    -> q k v lam o_branch lse dout dq dk dv dlam cu_seqlens B max_seqlen T Hq Hkv D window sink workspace workspace.n
+    => dq dk dv dlam""")
 _DECODE_SINK = _entry("diffattn_v2_decode_window_sink", """q:bf16[B,Hq,D] kcache:bf16[B,Smax,Hkv,D]
     vcache:bf16[B,Smax,Hkv,D] seqlens:i32[B] lam:f32[B,Hq/2] #window #sink >out:bf16[B,Hq/2,D]
     -> q kcache vcache seqlens lam out B Smax Hq Hkv D window sink => out""")

@@ -216,9 +216,9 @@ __global__ void pad_offsets_kernel(const int* __restrict__ cu, int* __restrict__
 
 // The same with sinks, and the first partial slot of each sequence (slot_off[b], in units of
 // Hkv * sink_tiles slots): one warp scans both.
-__global__ void pad_offsets_sink_kernel(const int* __restrict__ cu, int* __restrict__ pad_off,
-                                        int* __restrict__ slot_off, int B, int gpairs, int sink_parts,
-                                        int part_steps) {
+__global__ void pad_offsets_sink_kernel(const int* cu, int* pad_off, int* slot_off, int B, int gpairs,
+                                        int sink_parts, int part_steps) {
+  pdl_wait();
   const int lane = threadIdx.x;
   int rows = 0, slots = 0;
   for (int b0 = 0; b0 < B; b0 += 32) {
@@ -303,10 +303,11 @@ preprocess_varlen_kernel(const __nv_bfloat16* __restrict__ dout, const __nv_bflo
 // with one warp per row as above, 30.6 with each row's lse and lambda loaded when its sums were done).
 template <bool kVarlen>
 __global__ void __launch_bounds__(256, 4)
-preprocess_sink_kernel(const __nv_bfloat16* __restrict__ dout, const float* __restrict__ o_branch,
-                       const float* __restrict__ lse, const float* __restrict__ lambda, float* __restrict__ stats,
-                       float* __restrict__ dlam, const int* __restrict__ cu, const int* __restrict__ pad_off, int B,
+preprocess_sink_kernel(const __nv_bfloat16* dout, const float* o_branch,
+                       const float* lse, const float* lambda, float* stats,
+                       float* dlam, const int* cu, const int* pad_off, int B,
                        int S, int S_pad, int n_pairs) {
+  pdl_wait();
   __shared__ float rec[kStatArrays * kStatBlock];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks = S_pad / kStatBlock;
@@ -324,15 +325,15 @@ preprocess_sink_kernel(const __nv_bfloat16* __restrict__ dout, const float* __re
     int lo = 0, hi = B;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(pad_off + mid) <= i0) lo = mid; else hi = mid - 1;
+      if (pad_off[mid] <= i0) lo = mid; else hi = mid - 1;
     }
     b = lo;
     n = 0;
     base = 0;
     if (b < B) {
-      i0 -= __ldg(pad_off + b);
-      base = static_cast<size_t>(__ldg(cu + b));
-      n = __ldg(cu + b + 1) - static_cast<int>(base);
+      i0 -= pad_off[b];
+      base = static_cast<size_t>(cu[b]);
+      n = cu[b + 1] - static_cast<int>(base);
     }
   }
   // lanes 0-15: lse of row l / 2, branch l % 2 of the warp's eight rows; 16-23: lambda of row l - 16
@@ -341,8 +342,8 @@ preprocess_sink_kernel(const __nv_bfloat16* __restrict__ dout, const float* __re
     const int r = lane < 16 ? lane >> 1 : lane & 7, i = i0 + 8 * warp + r;
     if (i < n) {
       const size_t at = (base + i) * n_pairs + pair;
-      if (lane < 16) term = __ldg(lse + at * 2 + (lane & 1));
-      else if (lane < 24) term = __ldg(lambda + at);
+      if (lane < 16) term = lse[at * 2 + (lane & 1)];
+      else if (lane < 24) term = lambda[at];
     } else if (lane < 16) {
       term = INFINITY;  // a row past the sequence: its probabilities are exactly 0
     }
@@ -876,6 +877,7 @@ dkdv_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 constexpr int kSumThreads = 256;
 template <bool kVarlen>
 __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const Params p) {
+  pdl_wait();
   const int g = static_cast<int>(blockIdx.x) % p.Hkv, b = static_cast<int>(blockIdx.x) / p.Hkv;
   const int tile = static_cast<int>(blockIdx.y), k0 = tile * 128;
   int S = p.S, tok0 = 0;
@@ -1262,8 +1264,9 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     if (o_branch_f32) {
       int* slot_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(workspace) +
                                              backward_varlen_workspace_bytes(B, total_tokens, Hq));
-      pad_offsets_sink_kernel<<<1, 32, 0, stream>>>(cu_seqlens, pad_off, slot_off, B, Hq / Hkv / 2, plan.sink_parts,
-                                                    plan.part_steps);
+      e = launch_chained(pad_offsets_sink_kernel, dim3(1), dim3(32), 0, 0, stream, cu_seqlens, pad_off, slot_off, B,
+                         Hq / Hkv / 2, plan.sink_parts, plan.part_steps);
+      if (e != cudaSuccess) return e;
       p.slot_off = slot_off;
     } else {
       pad_offsets_kernel<<<1, 32, 0, stream>>>(cu_seqlens, pad_off, B);
@@ -1271,10 +1274,12 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long warps = static_cast<long long>(S_pad) * n_pairs;
-    if (o_branch_f32)
-      preprocess_sink_kernel<true><<<static_cast<unsigned>(warps / kStatBlock), 256, 0, stream>>>(
-          dout, o_branch_f32, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S, S_pad, n_pairs);
-    else
+    if (o_branch_f32) {
+      e = launch_chained(preprocess_sink_kernel<true>, dim3(static_cast<unsigned>(warps / kStatBlock)), dim3(256), 0, 0,
+                         stream, dout, o_branch_f32, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S, S_pad,
+                         n_pairs);
+      if (e != cudaSuccess) return e;
+    } else
       preprocess_varlen_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
           dout, o_branch, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S_pad, n_pairs);
     p.S_pad = S_pad;
@@ -1282,10 +1287,12 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   } else {
     const int S_pad = (S + kRowPad - 1) / kRowPad * kRowPad;
     const long long warps = static_cast<long long>(B) * S_pad * n_pairs;
-    if (o_branch_f32)
-      preprocess_sink_kernel<false><<<static_cast<unsigned>(warps / kStatBlock), 256, 0, stream>>>(
-          dout, o_branch_f32, lse, lambda, workspace, dlambda, nullptr, nullptr, B, S, S_pad, n_pairs);
-    else
+    if (o_branch_f32) {
+      e = launch_chained(preprocess_sink_kernel<false>, dim3(static_cast<unsigned>(warps / kStatBlock)), dim3(256), 0, 0,
+                         stream, dout, o_branch_f32, lse, lambda, workspace, dlambda, nullptr, nullptr, B, S, S_pad,
+                         n_pairs);
+      if (e != cudaSuccess) return e;
+    } else
       preprocess_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
           dout, o_branch, lse, lambda, workspace, dlambda, B, S, S_pad, n_pairs);
     p.S_pad = S_pad;
@@ -1338,8 +1345,9 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
       if (r != cudaSuccess) return r;
       // only the tiles that may have been split
       const int split_tiles = plan.tile_parts > 1 ? p.n_tiles : (plan.sink_parts > 1 ? plan.sink_tiles : 0);
-      if (split_tiles > 0) ksum<<<dim3(B * Hkv, split_tiles, 128 / 16), kSumThreads, 0, stream>>>(p);
-      return cudaGetLastError();
+      if (split_tiles > 0)
+        return launch_chained(ksum, dim3(B * Hkv, split_tiles, 128 / 16), dim3(kSumThreads), 0, 0, stream, p);
+      return cudaSuccess;
     };
     return cu_seqlens ? run_sink(backward_sink_sm100<true>, sum_parts_kernel<true>)
                       : run_sink(backward_sink_sm100<false>, sum_parts_kernel<false>);

@@ -16,6 +16,9 @@
 //                                            where k is given
 //                        #n  !flag           an integer, a truth value
 //                        %sections           a sequence of ints: pointer, %.n entries, %.sum
+//                        @ws(B,S,..)         a workspace, two Python arguments: the address of the C
+//                                            function that gives its bytes for these sizes, and a tensor
+//                                            or None (allocated); ws is its pointer, ws.n its bytes
 //   "->" C arguments     names of tensors (data pointers), sizes, scalars, io (dtype code), %, %.n
 //   "=>" results         one tensor, or a tuple
 //
@@ -42,7 +45,7 @@ namespace {
 
 constexpr int kMaxSyms = 32, kMaxTensors = 16, kMaxArgs = 40, kMaxSeq = 8;
 
-enum class Kind { kTensor, kOut, kInt, kFlag, kSeq };
+enum class Kind { kTensor, kOut, kInt, kFlag, kSeq, kSizeFn, kWork };
 enum class Layout { kContiguous, kHeads, kAlike };
 enum class Type { kBf16, kF32, kI32, kIo, kAny };
 
@@ -63,6 +66,7 @@ struct Item {
   int tensor = -1;     // index among the tensors
   int sym = -1;        // the symbol of a scalar, of a sequence's length, or of a layout's stride or size
   int sum = -1;        // the symbol of a sequence's sum
+  std::vector<int> sizes;  // the symbols that a workspace's size function takes
 };
 
 struct CArg {
@@ -132,6 +136,27 @@ Entry parse(const std::string& name, const std::string& spec) {
           it.sym = sym_of(e, "%.n", true);
           it.sum = sym_of(e, "%.sum", true);
         }
+        e.items.push_back(it);
+        continue;
+      }
+      if (w[0] == '@') {
+        const size_t open = w.find('('), close = w.find(')');
+        Item fn;
+        fn.kind = Kind::kSizeFn;
+        fn.name = w.substr(1, open - 1) + " size function";
+        e.items.push_back(fn);
+        it.kind = Kind::kWork;
+        it.name = w.substr(1, open - 1);
+        it.tensor = e.n_tensors++;
+        it.sym = sym_of(e, it.name + ".n", true);
+        std::string dims = w.substr(open + 1, close - open - 1);
+        for (size_t i = 0; i < dims.size();) {
+          size_t j = dims.find(',', i);
+          if (j == std::string::npos) j = dims.size();
+          it.sizes.push_back(sym_of(e, dims.substr(i, j - i), false));
+          i = j + 1;
+        }
+        TORCH_CHECK(e.n_tensors <= kMaxTensors && it.sizes.size() <= 8, "binding: malformed workspace in ", name);
         e.items.push_back(it);
         continue;
       }
@@ -226,6 +251,13 @@ struct Call {
       case Type::kIo: return io;
       default: return any;
     }
+  }
+
+  // a tensor of the current stream's pool is used on another
+  void record(const at::Tensor& x, cudaStream_t stream) const {
+    c10::cuda::CUDACachingAllocator::recordStream(
+        x.storage().data_ptr(), stream ? c10::cuda::getStreamFromExternal(stream, device.index())
+                                       : c10::cuda::getDefaultCUDAStream(device.index()));
   }
 
   bool take(const Item& it, PyObject* o) {
@@ -434,10 +466,34 @@ PyObject* invoke(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
     c.t[it.tensor] =
         at::detail::empty_cuda(at::IntArrayRef(sizes.data(), it.dims.size()), c.type_of(it), c.device, std::nullopt);
     if (it.layout == Layout::kHeads) c.val[it.sym] = sizes[1] * sizes[2];
-    if (so != Py_None)
-      c10::cuda::CUDACachingAllocator::recordStream(
-          c.t[it.tensor].storage().data_ptr(),
-          stream ? c10::cuda::getStreamFromExternal(stream, dev) : c10::cuda::getDefaultCUDAStream(dev));
+    if (so != Py_None) c.record(c.t[it.tensor], stream);
+  }
+  for (size_t i = 0; i < e.items.size(); ++i) {
+    const Item& it = e.items[i];
+    if (it.kind != Kind::kWork) continue;
+    std::array<int64_t, 8> a8{};
+    for (size_t k = 0; k < it.sizes.size(); ++k) a8[k] = c.val[it.sizes[k]];
+    void* size_fn = PyLong_AsVoidPtr(a[i - 1]);
+    if (PyErr_Occurred()) return nullptr;
+    const int64_t need = reinterpret_cast<int64_t (*)(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t,
+                                                      int64_t)>(size_fn)(a8[0], a8[1], a8[2], a8[3], a8[4], a8[5],
+                                                                         a8[6], a8[7]);
+    if (a[i] == Py_None) {
+      const int64_t bytes = std::max<int64_t>(need, 16);
+      c.t[it.tensor] = at::detail::empty_cuda(at::IntArrayRef(&bytes, 1), at::kByte, c.device, std::nullopt);
+      if (so != Py_None) c.record(c.t[it.tensor], stream);
+    } else {
+      if (!THPVariable_Check(a[i])) {
+        PyErr_Format(PyExc_TypeError, "%s: expected a tensor", it.name.c_str());
+        return nullptr;
+      }
+      c.t[it.tensor] = THPVariable_Unpack(a[i]);
+      if (c.t[it.tensor].device() != c.device || !c.t[it.tensor].is_contiguous()) {
+        PyErr_Format(PyExc_ValueError, "%s: expected a contiguous tensor on %s", it.name.c_str(), c.device.str().c_str());
+        return nullptr;
+      }
+    }
+    c.val[it.sym] = static_cast<int64_t>(c.t[it.tensor].nbytes());
   }
   std::array<int64_t, kMaxArgs> words{};
   size_t n = 0;
