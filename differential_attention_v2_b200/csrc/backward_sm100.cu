@@ -527,8 +527,8 @@ __device__ __forceinline__ size_t partial_slot(const Params& p, int b, int g, in
     // a sequence has room for the parts of its first tile, its longest
     int first = b * p.sink_parts, room = p.sink_parts;
     if (kVarlen) {
-      const int n = __ldg(p.cu_seqlens + b + 1) - __ldg(p.cu_seqlens + b);
-      first = __ldg(p.slot_off + b);
+      const int n = *(p.cu_seqlens + b + 1) - *(p.cu_seqlens + b);
+      first = *(p.slot_off + b);
       room = parts_of((n + 63) / 64 * (p.Hq / p.Hkv / 2), p.sink_parts, p.part_steps);
     }
     return (static_cast<size_t>(first) * p.Hkv + static_cast<size_t>(g) * room) * p.sink_tiles +
@@ -627,11 +627,11 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmQ, const CUtensorM
   int S = p.S, tok0 = 0, tb = b, srow0 = 0;
   size_t sb = static_cast<size_t>(b) * n_pairs;
   if (kVarlen) {
-    tok0 = __ldg(p.cu_seqlens + b);
-    S = __ldg(p.cu_seqlens + b + 1) - tok0;
+    tok0 = ld_in<kSink>(p.cu_seqlens + b);
+    S = ld_in<kSink>(p.cu_seqlens + b + 1) - tok0;
     tb = 0;
     sb = 0;
-    srow0 = __ldg(p.pad_off + b);
+    srow0 = ld_in<kSink>(p.pad_off + b);
   }
   if (k0 >= S) return;  // uniform over the CTA: the key tile lies past the sequence's end
   const size_t row_base = kVarlen ? static_cast<size_t>(tok0) : static_cast<size_t>(b) * p.S;
@@ -849,7 +849,7 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmQ, const CUtensorM
       const int d0 = (128 / kGroups) * cg;
       const size_t off = ((row_base + (key < S ? key : 0)) * p.Hkv + g) * HD + d0;
       // rows of the whole launch: B x S, or the packed sequences' total
-      const size_t total_rows = kVarlen ? static_cast<size_t>(__ldg(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
+      const size_t total_rows = kVarlen ? static_cast<size_t>(ld_in<kSink>(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
       const bool valid = key < S && checked(off + 128 / kGroups <= total_rows * p.Hkv * HD, p.err);
       if (kSink && parts > 1) {
         float* dst = p.partial + partial_slot<kVarlen>(p, b, g, tile, part, parts) * kSlotFloats + r * HD + d0;
@@ -883,8 +883,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const Params p) 
   int S = p.S, tok0 = 0;
   size_t row_base = static_cast<size_t>(b) * p.S;
   if (kVarlen) {
-    tok0 = __ldg(p.cu_seqlens + b);
-    S = __ldg(p.cu_seqlens + b + 1) - tok0;
+    tok0 = *(p.cu_seqlens + b);
+    S = *(p.cu_seqlens + b + 1) - tok0;
     row_base = static_cast<size_t>(tok0);
   }
   const int r0 = k0 + 16 * static_cast<int>(blockIdx.z);
@@ -939,11 +939,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
   int S = p.S, tok0 = 0, tb = b, srow0 = 0;
   size_t sb = static_cast<size_t>(b) * n_pairs;
   if (kVarlen) {
-    tok0 = __ldg(p.cu_seqlens + b);
-    S = __ldg(p.cu_seqlens + b + 1) - tok0;
+    tok0 = ld_in<kSink>(p.cu_seqlens + b);
+    S = ld_in<kSink>(p.cu_seqlens + b + 1) - tok0;
     tb = 0;
     sb = 0;
-    srow0 = __ldg(p.pad_off + b);
+    srow0 = ld_in<kSink>(p.pad_off + b);
   }
   if (m0 >= S) return;  // uniform over the CTA: the row tile lies past the sequence's end
   const size_t row_base = kVarlen ? static_cast<size_t>(tok0) : static_cast<size_t>(b) * p.S;
@@ -1082,11 +1082,11 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
     const int sr = srow0 + qi;  // this row in the row terms (past the sequence: -lse = -inf)
     // (with sinks query 0 too: it sees one key, so its dS is 0 and dP - E is only rounding)
     const bool lone = kSink && qi == 0;
-    const float nl1 = lone ? -INFINITY : __ldg(p.stats + stat_index(bp, p.S_pad, sr, 0));
-    const float nl2 = lone ? -INFINITY : __ldg(p.stats + stat_index(bp, p.S_pad, sr, 1));
-    const uint64_t ne1 = f2_pack(__ldg(p.stats + stat_index(bp, p.S_pad, sr, 2)), __ldg(p.stats + stat_index(bp, p.S_pad, sr, 2)));
-    const uint64_t ne2 = f2_pack(__ldg(p.stats + stat_index(bp, p.S_pad, sr, 3)), __ldg(p.stats + stat_index(bp, p.S_pad, sr, 3)));
-    const float nlam_s = __ldg(p.stats + stat_index(bp, p.S_pad, sr, 4));
+    const float nl1 = lone ? -INFINITY : ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 0));
+    const float nl2 = lone ? -INFINITY : ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 1));
+    const uint64_t ne1 = f2_pack(ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 2)), ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 2)));
+    const uint64_t ne2 = f2_pack(ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 3)), ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 3)));
+    const float nlam_s = ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 4));
     const uint64_t nl1_2 = f2_pack(nl1, nl1), nl2_2 = f2_pack(nl2, nl2), nlam = f2_pack(nlam_s, nlam_s);
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     for (int t = 0; ok && t < n_steps; ++t) {
@@ -1163,7 +1163,7 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
       tc_fence_after();
       const int d0 = (128 / kGroups) * cg;
       const size_t off = ((row_base + (qi < S ? qi : 0)) * p.Hq + 2 * pair) * HD + d0;
-      const size_t total_rows = kVarlen ? static_cast<size_t>(__ldg(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
+      const size_t total_rows = kVarlen ? static_cast<size_t>(ld_in<kSink>(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
       const bool valid = qi < S && checked(off + HD + 128 / kGroups <= total_rows * p.Hq * HD, p.err);
       store_row(trow + kTmAcc0 + d0, p.dq + off, p.scale, valid);
       store_row(trow + kTmAcc1 + d0, p.dq + off + HD, p.scale, valid);
@@ -1181,7 +1181,8 @@ dq_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtens
 
 // The sink form's tile kernels as one launch: n_kv CTAs of dK/dV, then those of dQ, which fill the
 // SMs that the last wave of the first leaves idle (both take a whole SM; a window makes their
-// numbers small: 280 and 512 CTAs for 4096 tokens).
+// numbers small: 280 and 512 CTAs for 4096 tokens; 352 us for both where they took 219 and 167 one
+// after the other; packed, 2,530 tokens, 64 against 62 and 34).
 template <bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 1)
 backward_sink_sm100(const __grid_constant__ CUtensorMap tmQ64, const __grid_constant__ CUtensorMap tmO64,
@@ -1189,6 +1190,7 @@ backward_sink_sm100(const __grid_constant__ CUtensorMap tmQ64, const __grid_cons
                     const __grid_constant__ CUtensorMap tmQ128, const __grid_constant__ CUtensorMap tmO128,
                     const __grid_constant__ CUtensorMap tmK64, const __grid_constant__ CUtensorMap tmV64,
                     const Params p, const int n_kv) {
+  pdl_wait();
   const int i = static_cast<int>(blockIdx.x);
   if (i < n_kv) {
     const int per = p.B * p.Hkv;
@@ -1340,8 +1342,8 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
       constexpr uint32_t smem = kKvSmem > kQSmem ? kKvSmem : kQSmem;
       cudaError_t r = cudaFuncSetAttribute(ktiles, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (r != cudaSuccess) return r;
-      ktiles<<<n_ctas, kThreads, smem, stream>>>(tmQ64, tmO64, tmK128, tmV128, tmQ128, tmO128, tmK64, tmV64, p, n_kv);
-      r = cudaGetLastError();
+      r = launch_chained(ktiles, dim3(n_ctas), dim3(kThreads), smem, 0, stream, tmQ64, tmO64, tmK128, tmV128, tmQ128,
+                         tmO128, tmK64, tmV64, p, n_kv);
       if (r != cudaSuccess) return r;
       // only the tiles that may have been split
       const int split_tiles = plan.tile_parts > 1 ? p.n_tiles : (plan.sink_parts > 1 ? plan.sink_tiles : 0);

@@ -222,8 +222,8 @@ __device__ __forceinline__ bool work_item(const Params& p, int k, WorkItem& w, S
   w.tok0 = 0;
   w.tb = w.b;
   if (kVarlen) {
-    w.tok0 = __ldg(p.cu_seqlens + w.b);
-    w.S = __ldg(p.cu_seqlens + w.b + 1) - w.tok0;
+    w.tok0 = ld_in<kSink>(p.cu_seqlens + w.b);
+    w.S = ld_in<kSink>(p.cu_seqlens + w.b + 1) - w.tok0;
     w.tb = 0;
   }
   w.row_base = kVarlen ? static_cast<size_t>(w.tok0) : static_cast<size_t>(w.b) * p.S;
@@ -474,7 +474,12 @@ __device__ __forceinline__ void arrive_for_mma(uint32_t bar, int lane) {
 //   * each softmax warp of either CTA arrives once on the even CTA's P and O-read barriers;
 //   * a wait that gives up raises the abort flag of both CTAs; both CTAs leave through one
 //     cluster barrier, after every copy and commit addressed to them has landed.
-// kSink (with kWindow, one CTA per item): the first p.sink keys stay visible below the window.
+// kSink (with kWindow, one CTA per item): the first p.sink keys stay visible below the window. The sink
+// tiles come first, so that a row's running max starts at its sinks', then the window's. Bound as the
+// window form by each branch's chain of softmax and MMAs, and by its half-masked tiles: 2 x 4096 tokens,
+// 64/8 heads, window 1024, 4 sinks 295 us (819 TFLOP/s counted; ten 128-key tiles run for eight tiles'
+// worth of visible keys). A narrow form of a tile with few sinks (32 columns of softmax, two K-steps of
+// P V) measured 299 and is not built.
 // kFine (with kSink, training): P of the tiles that hold sinks enters P V as two bf16 terms, over S's
 // other 64 columns. The sinks' weights are most of a row's, and O_b's error through their rounding is
 // the backward's E = dO . O_b off by the same amount for all of the row's keys.
@@ -486,6 +491,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   using R = Ring<kPair>;
   constexpr int kStages = R::kStages;
   constexpr uint32_t kOffV = off_v<kPair>();
+  if constexpr (kSink) pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -530,7 +536,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     // and holds the counts meanwhile.
     int* nt = reinterpret_cast<int*>(l_xchg);
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
-      const int len = __ldg(p.cu_seqlens + b + 1) - __ldg(p.cu_seqlens + b);
+      const int len = ld_in<kSink>(p.cu_seqlens + b + 1) - ld_in<kSink>(p.cu_seqlens + b);
       nt[b] = min(max((len + BM - 1) / BM, 0), p.n_row_tiles);
     }
     __syncthreads();
@@ -855,10 +861,10 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       const size_t lam_off = (w.row_base + (qi < S ? qi : 0)) * n_pairs + w.pair;
       bool lam_ok = qi < S;
       if constexpr (kDebugBounds) {
-        const size_t rows = kVarlen ? static_cast<size_t>(__ldg(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
+        const size_t rows = kVarlen ? static_cast<size_t>(ld_in<kSink>(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
         lam_ok = lam_ok && checked(lam_off < rows * n_pairs, p.err);
       }
-      float lam_row = (!kLamFused && lam_ok) ? __ldg(p.lambda + lam_off) : 0.f;
+      float lam_row = (!kLamFused && lam_ok) ? ld_in<kSink>(p.lambda + lam_off) : 0.f;
       float m_run = -INFINITY;
       float l_run = 0.f;
       for (int it = 0; it < w.n_kv; ++it) {
@@ -980,7 +986,7 @@ diffattn_prefill_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       lx[br * BM + r] = l_run;
       // training forward: A_b = 2^(s * scale_log2 - lse) recomputes the probabilities later
       // rows of the whole launch: B x S, or the packed sequences' total
-      const size_t total_rows = kVarlen ? static_cast<size_t>(__ldg(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
+      const size_t total_rows = kVarlen ? static_cast<size_t>(ld_in<kSink>(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
       if (p.lse != nullptr && qi < S &&
           checked((w.row_base + qi) * p.Hq + 2 * w.pair + br < total_rows * p.Hq, p.err))
         p.lse[(w.row_base + qi) * p.Hq + 2 * w.pair + br] = (m_run == -INFINITY ? 0.f : m_run) + __log2f(l_run);
@@ -1207,6 +1213,8 @@ cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   // balances them (a static deal that includes the empty items measured 745 against 800
   // TFLOP/s for 8 sequences of 512-3584 tokens).
   const int n_ctas = (one_per_item || p.n_items < n_sms) ? p.n_items : n_sms;
+  if (p.sink > 0 || o_branch_f32 != nullptr)
+    return launch_chained(kernel, dim3(n_ctas), dim3(kThreads), kSmemBytes, 0, stream, tmQ, tmK, tmV, tmK, tmO, p);
   kernel<<<n_ctas, kThreads, kSmemBytes, stream>>>(tmQ, tmK, tmV, tmK, tmO, p);
   return cudaGetLastError();
 }

@@ -41,6 +41,13 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // __restrict__), whose loads a compiler may move ahead of the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A load of an input: through the read-only path, or (kPlain) in a kernel that begins with pdl_wait.
+template <bool kPlain, typename T>
+__device__ __forceinline__ T ld_in(const T* p) {
+  if constexpr (kPlain) return *p;
+  else return __ldg(p);
+}
+
 // ----------------------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
