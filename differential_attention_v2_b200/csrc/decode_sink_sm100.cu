@@ -407,16 +407,17 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
   }
 }
 
-// CTAs per (KV head, sequence): as many as fit the GPU at two CTAs per SM, but no more than there
-// are stages; 16 (a non-portable size, slow to place) only for long lists. Measured on B200 (us, 8
-// KV heads, 4 sinks; CTAs per cluster 1 / 2 / 4 / 8 / 16):
-//   B=1,  window 1024    16.6  11.3   8.6   7.7   8.8
-//   B=1,  window 32768    316   161    84    46    31
-//   B=8,  window 4096    45.6  27.9  26.6  32.5  56.3
-//   B=32, window 1024    28.5  33.4  45.4  71.4   162
+// CTAs per (KV head, sequence): as many as fit the GPU at two CTAs per SM, but no more than there are
+// groups of 64 keys; 16 (a non-portable size whose receive buffers leave one CTA per SM) only for long
+// lists and few clusters. Measured on B200 (us, 8 KV heads, 4 sinks; CTAs per cluster 1 / 2 / 4 / 8 / 16):
+//   B=1,  window 1024    15.0  10.9   9.3   7.8   9.0
+//   B=1,  window 32768    307   157    83    45    31
+//   B=8,  window 4096    44.4  27.9  28.0  32.7  55.1
+//   B=32, window 1024    27.4  32.4  45.1  67.7   155
+// (before the partials were stored ahead of the barrier, which took about 1 us off each).
 int cluster_size(long long units, int span) {
   int c = 1;
-  while (c < kMaxCluster && 2 * c * units <= 296 && span > c && (c < 8 || span >= 256)) c *= 2;
+  while (c < kMaxCluster && 2 * c * units <= (c < 8 ? 296 : 148) && span > c && (c < 8 || span >= 256)) c *= 2;
   return c;
 }
 

@@ -286,3 +286,44 @@ def test_a_serving_run(da):
             vc[live.item():] = float("nan")
     attend(*grow([4, 0, 9, 1, 2]))
     assert da.device_error() == 0
+
+
+def test_chained_calls_without_synchronisation(da):
+    """Steps queued one behind the other give the bits of steps with a wait after every call."""
+    B, Hq, Hkv, page, N, steps, window, sink = 6, 8, 2, 16, 90, 60, 70, 3
+    inv = 10000.0 ** (-torch.arange(64, device="cuda") / 64)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    toks = torch.randn(steps, B, Hq + 2 * Hkv, 128, generator=g, device="cuda").bfloat16()
+    lam = torch.rand(steps, B, Hq // 2, generator=g, device="cuda")
+    one = torch.ones(B, dtype=torch.int32, device="cuda")
+
+    def run(wait):
+        def done(x=None):
+            if wait:
+                torch.cuda.synchronize()
+            return x
+
+        pool = Pool(B, 16, N)
+        kc = torch.zeros(N, page, Hkv, 128, dtype=torch.bfloat16, device="cuda")
+        vc = torch.zeros_like(kc)
+        outs = []
+        for i in range(steps):
+            done(da.cache_extend(pool.table, pool.L, pool.refs, one, page))
+            q, k, v = toks[i].split([Hq, Hkv, Hkv], 1)
+            pos = done((pool.L[None] - 1).contiguous())
+            qr = done(da.rope_append_paged(q, k, v, pos, inv, (64,), kc, vc, pool.table, pool.L))
+            outs.append(done(da.decode_paged(qr * 1.0, kc, vc, pool.table, pool.L, lam[i], window=window, sink=sink)))
+            done(da.cache_trim(pool.table, pool.L, pool.refs, page, window, sink))
+            if i == 30:
+                done(da.cache_free(pool.table, pool.L, pool.refs, _ints([1, 4])))
+                c, _ = done(da.cache_fork(pool.table, pool.L, pool.refs, _ints([0, 5]), _ints([1, 4]), page))
+                done(da.cache_copy_pages(kc, vc, c))
+                pool.table, pool.refs, m, _ = done(da.cache_compact(pool.table, pool.refs))
+                done(da.cache_copy_pages(kc, vc, m))
+        torch.cuda.synchronize()
+        return torch.stack(outs), pool.table, pool.refs, pool.L, kc, vc
+
+    ref = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), ref))
+    assert da.device_error() == 0

@@ -297,6 +297,68 @@ def test_decode_clamps_lengths_to_the_cache(da):
     assert torch.equal(out, ref)
 
 
+def test_decode_of_a_long_window_by_sixteen_ctas(da):
+    """One sequence and one KV head over more than 16,384 keys: the largest cluster."""
+    inp = _decode_inputs(8, 1, [20011], seed=16)
+    ref = ora.decode(inp["q"], inp["kcache"], inp["vcache"], inp["seqlens"], inp["lam"], window=18000, sink=40)
+    d = {k: v.cuda() for k, v in inp.items() if isinstance(v, torch.Tensor)}
+    out = da.decode(d["q"], d["kcache"], d["vcache"], d["seqlens"], d["lam"], window=18000, sink=40)
+    _ok(da)
+    bf16_close(out, ref, "long window")
+
+
+def test_a_cache_past_32_bits(da):
+    """Pages whose elements lie behind 2^31: append, copy and decode there."""
+    page, Hkv, Hq, N = 64, 8, 16, 40000
+    kc = torch.empty(N, page, Hkv, 128, dtype=torch.bfloat16, device="cuda")  # 5.2 GB
+    vc = torch.empty_like(kc)
+    n = 100
+    table = torch.tensor([[N - 1, N - 3]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q, k, v = r(n, Hq, 128), r(n, Hkv, 128), r(n, Hkv, 128)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    inv = 10000.0 ** (-torch.arange(64, device="cuda") / 64)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    qr = da.rope_append_paged(q, k, v, pos, inv, (64,), kc, vc, table, lens, cu_seqlens=cu)
+    kr = da.rope(k, None, pos, inv, (64,))[0]
+    lam = torch.rand(1, Hq // 2, generator=g, device="cuda")
+    ref = ora.decode(qr[-1:].cpu(), kr[None].cpu(), v[None].cpu(), [n], lam.cpu(), window=50, sink=4)
+    last = qr[-1:].contiguous()
+    bf16_close(da.decode_paged(last, kc, vc, table, lens, lam, window=50, sink=4), ref, "behind 2^31")
+    copies = torch.tensor([[N - 1, N - 2], [N - 3, 5]], dtype=torch.int32, device="cuda")
+    da.cache_copy_pages(kc, vc, copies)
+    moved = torch.tensor([[N - 2, 5]], dtype=torch.int32, device="cuda")
+    bf16_close(da.decode_paged(last, kc, vc, moved, lens, lam, window=50, sink=4), ref, "copied")
+    _ok(da)
+
+
+def test_calls_from_two_threads(da):
+    """The binding gives up the interpreter lock during a call; each thread has its own stream."""
+    import threading
+
+    inp = _decode_inputs(16, 2, [900, 450, 1, 777], seed=3)
+    d = [inp[n].cuda() for n in ("q", "kcache", "vcache", "seqlens", "lam")]
+    ref = da.decode(*d, window=300, sink=6)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(200):
+                if not torch.equal(da.decode(*d, window=300, sink=6), ref):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _ok(da)
+    assert not bad
+
+
 def test_decode_in_graphs_and_on_two_streams(da):
     """Two captured decodes and an eager one share nothing: replayed together they give their bits."""
     cases = []
@@ -359,6 +421,14 @@ def test_refusals(da):
         da.backward(*x, ob.bfloat16(), lse, d["dout"], window=8, sink=1)
     with pytest.raises(da.DiffAttnError):
         da.backward(*x, ob, lse, d["dout"], window=8, sink=1, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        da.prefill_window(*x, 2**40, sink=1)
+    with pytest.raises(TypeError):
+        da.prefill_window(*x, 8.5, sink=1)
+    with pytest.raises(TypeError):
+        da.prefill_window(None, *x[1:], 8, sink=1)
+    with pytest.raises(ValueError):
+        da.prefill_window(*x, 8, sink=1, out=torch.empty(1, 64, 128, 4, dtype=torch.bfloat16, device="cuda").mT)
     n = torch.ones(1, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         da.decode(d["q"][:, 0].contiguous(), d["k"], d["v"], n, d["lam"][:, 0].contiguous(), sink=1)
