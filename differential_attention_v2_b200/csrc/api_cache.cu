@@ -39,8 +39,9 @@ int rope_common(da2::RopeParams* p, const int32_t* positions, const float* inv_f
   return DA2_OK;
 }
 
+// (2^30 pages and tokens: page and token numbers plus a CTA's stride stay inside an int)
 bool pool_ok(int B, int max_pages, int page_shift, int num_pages) {
-  return B >= 0 && max_pages > 0 && page_shift >= 0 && num_pages > 0 &&
+  return B >= 0 && max_pages > 0 && page_shift >= 0 && num_pages > 0 && num_pages <= (1 << 30) &&
          (static_cast<long long>(max_pages) << page_shift) <= (1LL << 30);
 }
 
@@ -124,7 +125,8 @@ int diffattn_v2_cache_extend(int32_t* block_table, int32_t* seqlens, int32_t* re
   if (!pool_ok(B, max_pages, shift, num_pages)) return DA2_ERR_INVALID;
   if (B == 0) return DA2_OK;
   if (!ints_ok(block_table, seqlens, refs, n_new, result)) return DA2_ERR_INVALID;
-  if (B > da2::kMaxCacheSeqs) return DA2_ERR_UNSUPPORTED;
+  // (the pages that all sequences ask for are summed in an int)
+  if (B > da2::kMaxCacheSeqs || static_cast<long long>(B) * max_pages > 2147483647LL) return DA2_ERR_UNSUPPORTED;
   return status_of(da2::launch_cache_extend(block_table, seqlens, refs, n_new, result, B, max_pages, shift, num_pages,
                                             reinterpret_cast<cudaStream_t>(stream)));
 }

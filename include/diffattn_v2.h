@@ -576,13 +576,15 @@ DA2_API int diffattn_v2_rope_append_paged(const void* q, const void* k, const vo
  *   block_table int32 [B, max_pages]  page of each logical page, -1 none
  *   seqlens     int32 [B]             tokens of each sequence (0: an empty row)
  *   refs        int32 [num_pages]     table entries that name the page; 0 = free
+ * At most 2^30 pages, and 2^30 tokens in a row of the table.
  * One table serves every layer with the same window and sinks. Free pages are taken lowest index
  * first, so the result of a call is unique. result int32 [1] (device) tells what happened; a call
  * that refuses changes nothing else but `copies`, which it fills with -1.
  *
  * extend: n_new[b] (negative: 0) more tokens for every sequence: seqlens grows, and logical pages
  *   that did not exist get a page, in the order of (b, logical page). result: pages taken, or -1:
- *   the pool has too few free pages, or a sequence would need more than max_pages. B <= 2048.
+ *   the pool has too few free pages, or a sequence would need more than max_pages. B <= 2048,
+ *   B * max_pages < 2^31.
  * fork: row children[i] becomes a second owner of what row parents[i] holds: whole pages are
  *   shared, a partly filled last page gets a page of its own, and copies[i] = (old page, new page)
  *   lists the copy that diffattn_v2_cache_copy_pages has to make, once per layer; (-1, -1): none.

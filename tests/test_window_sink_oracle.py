@@ -186,3 +186,16 @@ def test_cache_refusals(lib):
     assert y(A[0], A[1], A[2], 3, 9, 24, None) == UNS and y(A[0], A[1] + 8, A[2], 3, 9, 64, None) == INV
     assert y(A[0], A[1], A[2], 0, 9, 64, None) == OK
 
+
+def test_cache_size_limits(lib):
+    """Index arithmetic in 32 bits: pools of more than 2^30 pages, and tables whose entries cannot be
+    counted in an int, are refused."""
+    e, fk, tr, fr, c = (getattr(lib, "diffattn_v2_cache_" + n) for n in ("extend", "fork", "trim", "free", "compact"))
+    big = (1 << 30) + 1
+    assert e(*A[:5], 4, 8, 16, big, None) == INV
+    assert fk(*A[:7], 2, 4, 8, 16, big, None) == INV
+    assert tr(*A[:4], 4, 8, 16, big, 64, 4, None) == INV
+    assert fr(*A[:5], 1, 4, 8, big, None) == INV
+    assert c(*A[:6], 4, 8, big, None) == INV
+    assert e(*A[:5], 2048, 1 << 20, 8, 9, None) == UNS  # 2^31 entries
+    assert e(*A[:5], 0, 1 << 20, 8, 9, None) == OK
