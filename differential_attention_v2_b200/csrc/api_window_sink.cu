@@ -70,6 +70,10 @@ int backward(const void* q, const void* k, const void* v, const float* lambda, c
   if ((static_cast<long long>(S) + 127) / 128 > 60000 || padded > 2147483647LL ||
       padded * (Hq / 2) > 4LL * 2147483647LL || static_cast<long long>(B) * Hq > 2147483647LL)
     return DA2_ERR_UNSUPPORTED;
+  // The tile kernel's CTAs are counted in an int, and every sequence has those of the longest one: at
+  // most half of this product for dQ, as many for the key tiles, and for the parts of split tiles
+  // about 600 per 64-row query block of the longest sequence (72e6 of those).
+  if ((static_cast<long long>(S) + 127) / 128 * B * Hq > 2000000000LL) return DA2_ERR_UNSUPPORTED;
   int* err = nullptr;
   if (da2::device_error_word(&err) != cudaSuccess) return DA2_ERR_CUDA;
   const int rows = packed ? total : S, batch = packed ? 1 : B;

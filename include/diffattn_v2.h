@@ -483,7 +483,9 @@ DA2_API int diffattn_v2_prefill_varlen_window_sink(const void* q, const void* k,
  * dS = A (dO.v_j - dO.O_b) is a small difference of large terms that a bf16 O_b would drown. For the
  * same reason the products over (the first 512) sink keys keep their weights and dS as two bf16 terms,
  * so that `out` here is nearer the exact value than the inference call's, not bit for bit the same. A
- * query that sees a single key has a constant softmax: its dq, and its part of dk, are exactly 0.
+ * sequence's first query sees a single key, so its softmax is constant: its dq, and its part of dk, are
+ * exactly 0. Packed sequences each launch the longest one's tiles: DA2_ERR_UNSUPPORTED where
+ * B * Hq * ceil(max_seqlen / 128) passes 2e9.
  * The workspace needs no initialisation; calls that share one must not overlap on the GPU. The
  * result is deterministic (no atomics).
  */

@@ -199,3 +199,13 @@ def test_cache_size_limits(lib):
     assert c(*A[:6], 4, 8, big, None) == INV
     assert e(*A[:5], 2048, 1 << 20, 8, 9, None) == UNS  # 2^31 entries
     assert e(*A[:5], 0, 1 << 20, 8, 9, None) == OK
+
+
+def test_backward_launch_limits(lib):
+    """Many packed sequences beside a very long one: a grid whose CTAs cannot be counted in an int is
+    refused (its count used to wrap)."""
+    g = lib.diffattn_v2_backward_varlen_window_sink
+    x = A[:11]
+    # 16384 sequences of at most 2^20 tokens, 32 pairs: 2^32 query tiles
+    assert g(*x, A[11], 16384, 1 << 20, 1 << 21, 64, 8, 128, 1024, 4, A[12], 1 << 60, None) == UNS
+    assert g(*x, A[11], 16384, 1 << 20, 1 << 21, 64, 8, 128, 1 << 20, 4, A[12], 1 << 60, None) == UNS
