@@ -23,9 +23,12 @@
 //   "=>" results         one tensor, or a tuple
 //
 // The last Python argument is the stream (None: the device's current one; a torch stream; a raw
-// handle), the last C argument its handle. Calls run on the tensors' device. Errors: TypeError for
-// dtypes, ValueError for shapes, devices and layouts; a status other than 0 goes to the callable
-// given to `on_error`.
+// handle), the last C argument its handle. What a call allocates comes from the memory pool of the
+// stream that it runs on: a block of the current stream's pool may still be in use by work queued
+// there, which the given stream does not wait for. Outputs are recorded on the current stream, where
+// the caller will read them. Calls run on the tensors' device. Errors: TypeError for dtypes,
+// ValueError for shapes, devices and layouts; a status other than 0 goes to the callable given to
+// `on_error`.
 
 #include <Python.h>
 
@@ -253,13 +256,6 @@ struct Call {
     }
   }
 
-  // a tensor of the current stream's pool is used on another
-  void record(const at::Tensor& x, cudaStream_t stream) const {
-    c10::cuda::CUDACachingAllocator::recordStream(
-        x.storage().data_ptr(), stream ? c10::cuda::getStreamFromExternal(stream, device.index())
-                                       : c10::cuda::getDefaultCUDAStream(device.index()));
-  }
-
   bool take(const Item& it, PyObject* o) {
     if (!THPVariable_Check(o)) {
       PyErr_Format(PyExc_TypeError, "%s: expected a tensor", it.name.c_str());
@@ -453,6 +449,12 @@ PyObject* invoke(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
     Py_DECREF(raw);
     if (PyErr_Occurred()) return nullptr;
   }
+  // from here on the call's stream is the current one, whose pool the allocator takes from
+  const c10::cuda::CUDAStream caller = c10::cuda::getCurrentCUDAStream(dev);
+  const bool elsewhere = stream != caller.stream();
+  c10::cuda::OptionalCUDAStreamGuard on_stream;
+  if (elsewhere)
+    on_stream.reset_stream(stream ? c10::cuda::getStreamFromExternal(stream, dev) : c10::cuda::getDefaultCUDAStream(dev));
   for (size_t i = 0; i < e.items.size(); ++i) {
     const Item& it = e.items[i];
     if (it.kind != Kind::kOut) continue;
@@ -466,7 +468,7 @@ PyObject* invoke(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
     c.t[it.tensor] =
         at::detail::empty_cuda(at::IntArrayRef(sizes.data(), it.dims.size()), c.type_of(it), c.device, std::nullopt);
     if (it.layout == Layout::kHeads) c.val[it.sym] = sizes[1] * sizes[2];
-    if (so != Py_None) c.record(c.t[it.tensor], stream);
+    if (elsewhere) c10::cuda::CUDACachingAllocator::recordStream(c.t[it.tensor].storage().data_ptr(), caller);
   }
   for (size_t i = 0; i < e.items.size(); ++i) {
     const Item& it = e.items[i];
@@ -481,7 +483,6 @@ PyObject* invoke(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
     if (a[i] == Py_None) {
       const int64_t bytes = std::max<int64_t>(need, 16);
       c.t[it.tensor] = at::detail::empty_cuda(at::IntArrayRef(&bytes, 1), at::kByte, c.device, std::nullopt);
-      if (so != Py_None) c.record(c.t[it.tensor], stream);
     } else {
       if (!THPVariable_Check(a[i])) {
         PyErr_Format(PyExc_TypeError, "%s: expected a tensor", it.name.c_str());

@@ -1,0 +1,154 @@
+"""Calls with an explicit stream. What a call allocates has to come from the memory pool of the stream that
+it runs on: the allocator hands out a block of the current stream's pool while work queued there may still
+use it, and the given stream does not wait for that work. The outputs, which the caller reads on its own
+stream, must not go back to the pool while work queued there still reads them."""
+import pytest
+import torch
+
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def da():
+    import differential_attention_v2_b200 as m
+
+    assert torch.cuda.is_available()
+    return m
+
+
+@pytest.fixture(scope="module")
+def x():
+    """Small inputs of every call below."""
+    case = workloads.PrefillCase(B=1, S=200, Hq=8, Hkv=2, D=128, seed=1)
+    d = {k: v.cuda() for k, v in workloads.make_prefill(case).items()}
+    d["dout"] = workloads.make_prefill_grad(case).cuda()
+    d["qkvl"] = tuple(d[n] for n in ("q", "k", "v", "lam"))
+    d["packed"] = tuple(t[0].contiguous() for t in d["qkvl"])
+    d["cu"] = torch.tensor([0, 150, 200], dtype=torch.int32, device="cuda")
+    d["step"] = (d["q"][:, -1].contiguous(), d["k"], d["v"], torch.tensor([200], dtype=torch.int32, device="cuda"),
+                 d["lam"][:, -1].contiguous())
+    d["pages"] = (d["step"][0], d["k"].view(25, 8, 2, 128), d["v"].view(25, 8, 2, 128),
+                  torch.arange(25, dtype=torch.int32, device="cuda").view(1, 25), *d["step"][3:])
+    d["pos"] = torch.arange(200, dtype=torch.int32, device="cuda")[None]
+    d["inv"] = torch.rand(64, device="cuda")
+    d["pool"] = (d["pages"][3].clone(), torch.tensor([200], dtype=torch.int32, device="cuda"),
+                 torch.ones(25, dtype=torch.int32, device="cuda"))
+    return d
+
+
+def _backward(da, x, s, **kw):
+    _, ob, lse = da.prefill_train(*x["qkvl"], **kw)
+    torch.cuda.synchronize()
+    return lambda: da.backward(*x["qkvl"], ob, lse, x["dout"], stream=s, **kw)
+
+
+def _backward_varlen(da, x, s, **kw):
+    _, ob, lse = da.prefill_varlen_train(*x["packed"], x["cu"], 150, **kw)
+    torch.cuda.synchronize()
+    return lambda: da.backward_varlen(*x["packed"], ob, lse, x["dout"][0], x["cu"], 150, stream=s, **kw)
+
+
+W = dict(window=50, sink=3)
+
+
+def _append(da, x, s):
+    k, v, cu = x["pages"][1].clone(), x["pages"][2].clone(), x["cu"][::2].contiguous()
+    torch.cuda.synchronize()
+    return lambda: da.rope_append_paged(x["q"][0], x["k"][0], x["v"][0], x["pos"], x["inv"], (64,), k, v,
+                                        *x["pages"][3:5], cu_seqlens=cu, stream=s)
+
+
+def _pages(call):
+    """A bookkeeping call that changes nothing: no new tokens, padding, a window of every key."""
+    def make(da, x, s):
+        none, zero = torch.full((1,), -1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        return lambda: call(da, x["pool"], none, zero, s)
+    return make
+
+
+SINK_ROPE_CACHE = {
+    "prefill_window": lambda da, x, s: lambda: da.prefill_window(*x["qkvl"], 50, sink=3, stream=s),
+    "prefill_varlen_window": lambda da, x, s: lambda: da.prefill_varlen_window(*x["packed"], x["cu"], 150, 50, sink=3,
+                                                                               stream=s),
+    "prefill_train": lambda da, x, s: lambda: da.prefill_train(*x["qkvl"], stream=s, **W),
+    "prefill_varlen_train": lambda da, x, s: lambda: da.prefill_varlen_train(*x["packed"], x["cu"], 150, stream=s, **W),
+    "backward": lambda da, x, s: _backward(da, x, s, **W),
+    "backward_varlen": lambda da, x, s: _backward_varlen(da, x, s, **W),
+    "decode": lambda da, x, s: lambda: da.decode(*x["step"], stream=s, **W),
+    "decode_paged": lambda da, x, s: lambda: da.decode_paged(*x["pages"], stream=s, **W),
+    "rope": lambda da, x, s: lambda: da.rope(x["q"][0], x["k"][0], x["pos"], x["inv"], (64,), stream=s),
+    "rope_append_paged": _append,
+    "cache_extend": _pages(lambda da, pool, none, zero, s: da.cache_extend(*pool, zero, 8, stream=s)),
+    "cache_fork": _pages(lambda da, pool, none, zero, s: da.cache_fork(*pool, zero, none, 8, stream=s)),
+    "cache_trim": _pages(lambda da, pool, none, zero, s: da.cache_trim(*pool, 8, 500, 3, stream=s)),
+    "cache_free": _pages(lambda da, pool, none, zero, s: da.cache_free(*pool, none, stream=s)),
+    "cache_compact": _pages(lambda da, pool, none, zero, s: da.cache_compact(pool[0], pool[2], stream=s)),
+}
+
+
+def _tensors(out):
+    return [t for t in (out if isinstance(out, (tuple, list)) else (out,)) if t is not None]
+
+
+def _pool_of(t):
+    """Handle of the stream whose pool holds t, and the state of its block."""
+    for seg in torch.cuda.memory_snapshot():
+        at = seg["address"]
+        for block in seg["blocks"]:
+            if at <= t < at + block["size"]:
+                return seg["stream"], block["state"]
+            at += block["size"]
+    raise AssertionError("not an allocated block")
+
+
+def _check_pool(call, s):
+    handle = s if isinstance(s, int) else s.cuda_stream
+    ref = _tensors(call())
+    torch.cuda.synchronize()
+    where = [_pool_of(t.data_ptr())[0] for t in ref if t.numel()]
+    assert where and all(w == handle for w in where), (where, handle)
+    # an output dropped while the caller's stream is busy stays out of the pool until that work is done
+    ptr = ref[0].data_ptr()
+    torch.cuda._sleep(100_000_000)  # about 50 ms
+    del ref
+    assert _pool_of(ptr)[1] == "active_pending_free"
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", SINK_ROPE_CACHE)
+def test_allocations_belong_to_the_given_stream(da, x, name, raw):
+    s = torch.cuda.Stream()
+    _check_pool(SINK_ROPE_CACHE[name](da, x, s.cuda_stream if raw else s), s)
+
+
+@pytest.mark.parametrize("name", ["backward", "backward_varlen"])
+def test_workspaces_belong_to_the_given_stream(da, x, name):
+    """Every allocation that the call makes, the workspace that it drops included."""
+    s = torch.cuda.Stream()
+    call = SINK_ROPE_CACHE[name](da, x, s)
+    torch.cuda.memory._record_memory_history(enabled="all", context=None, max_entries=10000, clear_history=True)
+    try:
+        out = call()
+        torch.cuda.synchronize()
+        trace = torch.cuda.memory._snapshot()["device_traces"][torch.cuda.current_device()]
+    finally:
+        torch.cuda.memory._record_memory_history(enabled=None)
+    made = [e["stream"] for e in trace if e["action"] == "alloc"]
+    assert len(made) > len(out) and all(h == s.cuda_stream for h in made), made
+
+
+def test_results_on_a_given_stream(da, x):
+    """The same bits as on the current stream, for torch streams, raw handles and the default stream."""
+    ref = _tensors(_backward(da, x, None, **W)())
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = _tensors(_backward(da, x, s, **W)())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert da.device_error() == 0
