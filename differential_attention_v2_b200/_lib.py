@@ -139,6 +139,13 @@ def _stream(stream, device):
     return int(stream)
 
 
+def _torch_stream(stream, device):
+    """A given stream as a torch stream."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -636,12 +643,11 @@ def rope_append_paged(q, k, v, positions, inv_freq, sections, kpages, vpages, bl
                    kpages, vpages, block_table, seqlens, cu_seqlens, q_out, interleaved, stream)
 
 
-def _no_pages(result, block_table, n, stream):
-    """The result of a bookkeeping call on nothing, which launches nothing: 0."""
-    if n == 0 or block_table.shape[0] == 0:
-        if result is None:
-            result = torch.empty(1, dtype=torch.int32, device=block_table.device)
-        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+def _of_nothing(result, nothing, stream):
+    """The result of a bookkeeping call, checked and allocated by it. One on nothing launches nothing:
+    its result is 0, written on the call's stream."""
+    if nothing:
+        with torch.cuda.stream(None if stream is None else _torch_stream(stream, result.device)):
             result.zero_()
     return result
 
@@ -650,9 +656,9 @@ def cache_extend(block_table, seqlens, refs, n_new, page_size, result=None, stre
     """n_new[b] more tokens for every sequence: seqlens grows and the pages that are missing are
     taken from the free ones (refs == 0), lowest first. Returns result int32 [1] on the device:
     pages taken, or -1 (too few free pages or a full row; nothing changed)."""
-    result = _no_pages(result, block_table, 1, stream)
-    return _invoke(_CACHE_EXTEND, LIB.addresses["diffattn_v2_cache_extend"], block_table, seqlens, refs, n_new, page_size,
-                   result, stream)
+    result = _invoke(_CACHE_EXTEND, LIB.addresses["diffattn_v2_cache_extend"], block_table, seqlens, refs, n_new,
+                     page_size, result, stream)
+    return _of_nothing(result, seqlens.numel() == 0, stream)
 
 
 def cache_fork(block_table, seqlens, refs, parents, children, page_size, copies=None, result=None, stream=None):
@@ -661,24 +667,24 @@ def cache_fork(block_table, seqlens, refs, parents, children, page_size, copies=
     where there is none; result int32 [1]: pages taken, -1 too few free pages, -2 a bad pair)."""
     if block_table.shape[0] == 0 and parents.numel() > 0:
         raise ValueError("parents: the table has no rows")
-    result = _no_pages(result, block_table, parents.numel(), stream)
-    return _invoke(_CACHE_FORK, LIB.addresses["diffattn_v2_cache_fork"], block_table, seqlens, refs, parents, children,
-                   page_size, copies, result, stream)
+    copies, result = _invoke(_CACHE_FORK, LIB.addresses["diffattn_v2_cache_fork"], block_table, seqlens, refs, parents,
+                             children, page_size, copies, result, stream)
+    return copies, _of_nothing(result, parents.numel() == 0, stream)
 
 
 def cache_trim(block_table, seqlens, refs, page_size, window, sink, result=None, stream=None):
     """Pages that hold neither one of the first `sink` keys nor one of the last `window` leave their
     sequence. Returns result int32 [1]: pages that became free."""
-    result = _no_pages(result, block_table, 1, stream)
-    return _invoke(_CACHE_TRIM, LIB.addresses["diffattn_v2_cache_trim"], block_table, seqlens, refs, page_size, window,
-                   sink, result, stream)
+    result = _invoke(_CACHE_TRIM, LIB.addresses["diffattn_v2_cache_trim"], block_table, seqlens, refs, page_size, window,
+                     sink, result, stream)
+    return _of_nothing(result, seqlens.numel() == 0, stream)
 
 
 def cache_free(block_table, seqlens, refs, seqs, result=None, stream=None):
     """The listed sequences (int32; negative entries are padding) give their pages back and become
     empty. Returns result int32 [1]: pages that became free, or -2 (an index >= B; nothing changed)."""
-    result = _no_pages(result, block_table, seqs.numel(), stream)
-    return _invoke(_CACHE_FREE, LIB.addresses["diffattn_v2_cache_free"], block_table, seqlens, refs, seqs, result, stream)
+    result = _invoke(_CACHE_FREE, LIB.addresses["diffattn_v2_cache_free"], block_table, seqlens, refs, seqs, result, stream)
+    return _of_nothing(result, seqs.numel() == 0 or seqlens.numel() == 0, stream)
 
 
 def cache_compact(block_table, refs, block_table_out=None, refs_out=None, moves=None, result=None, stream=None):

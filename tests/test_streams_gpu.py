@@ -152,3 +152,45 @@ def test_results_on_a_given_stream(da, x):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
     assert da.device_error() == 0
+
+
+NOTHING = {  # calls on nothing, which launch no kernel: (call, B)
+    "extend": (lambda da, pool, n, **kw: da.cache_extend(*pool, n, 8, **kw), 0),
+    "fork": (lambda da, pool, n, **kw: da.cache_fork(*pool, n, n, 8, **kw)[1], 3),
+    "trim": (lambda da, pool, n, **kw: da.cache_trim(*pool, 8, 4, 1, **kw), 0),
+    "free": (lambda da, pool, n, **kw: da.cache_free(*pool, n, **kw), 3),
+}
+
+
+@pytest.mark.parametrize("which", ["none", "torch", "raw", "default"])
+@pytest.mark.parametrize("name", NOTHING)
+def test_the_result_of_nothing_is_written_in_the_streams_order(da, name, which):
+    call, B = NOTHING[name]
+    ints = dict(dtype=torch.int32, device="cuda")
+    pool = (torch.full((B, 4), -1, **ints), torch.zeros(B, **ints), torch.zeros(5, **ints))
+    result, n = torch.zeros(1, **ints), torch.zeros(0, **ints)
+    torch.cuda.synchronize()
+    side = torch.cuda.default_stream() if which == "default" else torch.cuda.Stream()
+    given = {"none": None, "torch": side, "raw": side.cuda_stream, "default": 0}[which]
+    with torch.cuda.stream(side):  # a value that the call has to come after
+        torch.cuda._sleep(100_000_000)
+        result.fill_(7)
+    with torch.cuda.stream(side if which == "none" else torch.cuda.Stream()):
+        got = call(da, pool, n, result=result, stream=given)
+        fresh = call(da, pool, n, stream=given)
+    torch.cuda.synchronize()
+    assert got is result and got.tolist() == [0] and fresh.tolist() == [0]
+
+
+@pytest.mark.parametrize("name", NOTHING)
+def test_a_refused_result_keeps_its_value(da, name):
+    call, B = NOTHING[name]
+    ints = dict(dtype=torch.int32, device="cuda")
+    pool = (torch.full((B, 4), -1, **ints), torch.zeros(B, **ints), torch.zeros(5, **ints))
+    for bad, error in ((torch.full((1,), 7, device="cuda"), TypeError), (torch.full((2,), 7, **ints), ValueError)):
+        with pytest.raises(error):
+            call(da, pool, torch.zeros(0, **ints), result=bad)
+        assert bad.eq(7).all()
+    if name != "trim":  # (takes no list)
+        with pytest.raises(TypeError):
+            call(da, pool, [])
