@@ -146,6 +146,24 @@ def _torch_stream(stream, device):
     return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
 
 
+def _empty(stream, shape, dtype, device):
+    """An output or workspace of a call on `stream` (None: the current one), from that stream's memory
+    pool: a block of the current stream's pool may still be in use by work queued there, which the
+    given stream does not wait for. It is recorded on the current stream, where the caller reads it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.numel():
+        t.record_stream(caller)
+    return t
+
+
+def _empty_like(stream, t):
+    return _empty(stream, t.shape, dtype=t.dtype, device=t.device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -179,7 +197,7 @@ def prefill(q, k, v, lam, out=None, causal=True, stream=None):
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty((B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 4)
     st = LIB.diffattn_v2_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(out), B, S, Hq, Hkv, D,
                                  1 if causal else 0, _stream(stream, q.device))
@@ -199,7 +217,7 @@ def prefill_window(q, k, v, lam, window, out=None, stream=None, sink=None):
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty((B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 4)
     st = LIB.diffattn_v2_prefill_window(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(out), B, S, Hq, Hkv, D,
                                         int(window), _stream(stream, q.device))
@@ -218,7 +236,7 @@ def prefill_varlen(q, k, v, lam, cu_seqlens, max_seqlen, out=None, causal=True, 
     Hkv = k.shape[1]
     B = cu_seqlens.numel() - 1
     if out is None:
-        out = torch.empty((T, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (T, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 3)
     st = LIB.diffattn_v2_prefill_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(out), _ptr(cu_seqlens), B,
                                         int(max_seqlen), T, Hq, Hkv, D, 1 if causal else 0, _stream(stream, q.device))
@@ -241,7 +259,7 @@ def prefill_varlen_window(q, k, v, lam, cu_seqlens, max_seqlen, window, out=None
     Hkv = k.shape[1]
     B = cu_seqlens.numel() - 1
     if out is None:
-        out = torch.empty((T, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (T, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 3)
     st = LIB.diffattn_v2_prefill_varlen_window(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(out), _ptr(cu_seqlens), B,
                                                int(max_seqlen), T, Hq, Hkv, D, int(window), _stream(stream, q.device))
@@ -256,7 +274,7 @@ def prefill_f32(q, k, v, lam, out=None, causal=True, stream=None):
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty((B, S, Hq // 2, D), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, S, Hq // 2, D), dtype=torch.float32, device=q.device)
     _need(out, "out", torch.float32, 4)
     st = LIB.diffattn_v2_prefill_f32(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(out), B, S, Hq, Hkv, D,
                                      1 if causal else 0, _stream(stream, q.device))
@@ -278,11 +296,11 @@ def prefill_train(q, k, v, lam, out=None, o_branch=None, lse=None, causal=True, 
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
     if out is None:
-        out = torch.empty((B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     if o_branch is None:
-        o_branch = torch.empty((B, S, Hq, D), dtype=torch.bfloat16, device=q.device)
+        o_branch = _empty(stream, (B, S, Hq, D), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((B, S, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, S, Hq), dtype=torch.float32, device=q.device)
     _need(out, "out", torch.bfloat16, 4)
     _need(o_branch, "o_branch", torch.bfloat16, 4)
     _need(lse, "lse", torch.float32, 3)
@@ -316,16 +334,16 @@ def backward(q, k, v, lam, o_branch, lse, dout, causal=True, dq=None, dk=None, d
     _need(lse, "lse", torch.float32, 3)
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    dlam = torch.empty_like(lam) if dlam is None else dlam
+    dq = _empty_like(stream, q) if dq is None else dq
+    dk = _empty_like(stream, k) if dk is None else dk
+    dv = _empty_like(stream, v) if dv is None else dv
+    dlam = _empty_like(stream, lam) if dlam is None else dlam
     for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
         _need(t, n, torch.bfloat16, 4)
     _need(dlam, "dlam", torch.float32, 3)
     ws_bytes = backward_workspace_size(B, S, Hq)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
     if window is not None:
         st = LIB.diffattn_v2_backward_window(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(o_branch), _ptr(lse),
                                              _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dlam), B, S, Hq, Hkv, D,
@@ -356,9 +374,9 @@ def prefill_varlen_train(q, k, v, lam, cu_seqlens, max_seqlen, out=None, o_branc
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     B = cu_seqlens.numel() - 1
-    out = torch.empty((T, Hq // 2, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    o_branch = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if o_branch is None else o_branch
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    out = _empty(stream, (T, Hq // 2, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    o_branch = _empty(stream, (T, Hq, D), dtype=torch.bfloat16, device=q.device) if o_branch is None else o_branch
+    lse = _empty(stream, (T, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
     _need(out, "out", torch.bfloat16, 3)
     _need(o_branch, "o_branch", torch.bfloat16, 3)
     _need(lse, "lse", torch.float32, 2)
@@ -397,10 +415,10 @@ def backward_varlen(q, k, v, lam, o_branch, lse, dout, cu_seqlens, max_seqlen, c
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     B = cu_seqlens.numel() - 1
-    dq, dk, dv, dlam = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(lam)
+    dq, dk, dv, dlam = (_empty_like(stream, t) for t in (q, k, v, lam))
     ws_bytes = backward_varlen_workspace_size(B, T, Hq)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
     ws_given = workspace.numel() * workspace.element_size()
     if window is not None:
         st = LIB.diffattn_v2_backward_varlen_window(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(o_branch), _ptr(lse),
@@ -436,11 +454,11 @@ def decode(q, kcache, vcache, seqlens, lam, out=None, workspace=None, stream=Non
     B, Hq, D = q.shape
     Smax, Hkv = kcache.shape[1], kcache.shape[2]
     if out is None:
-        out = torch.empty((B, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 3)
     need = decode_workspace_size(B, Smax, Hq, Hkv, D)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(need, 16), dtype=torch.uint8, device=q.device)
     if window is not None:
         st = LIB.diffattn_v2_decode_window(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(seqlens), _ptr(lam), _ptr(out), B,
                                            Smax, Hq, Hkv, D, int(window), _ptr(workspace),
@@ -465,11 +483,11 @@ def decode_multi(q, kcache, vcache, seqlens, lam, out=None, workspace=None, stre
     B, T, Hq, D = q.shape
     Smax, Hkv = kcache.shape[1], kcache.shape[2]
     if out is None:
-        out = torch.empty((B, T, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, T, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 4)
     need = int(LIB.diffattn_v2_decode_multi_workspace_size(B, T, Smax, Hq, Hkv, D))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(need, 16), dtype=torch.uint8, device=q.device)
     st = LIB.diffattn_v2_decode_multi(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(seqlens), _ptr(lam), _ptr(out), B, T,
                                       Smax, Hq, Hkv, D, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                       _stream(stream, q.device))
@@ -496,11 +514,11 @@ def decode_paged(q, kpages, vpages, block_table, seqlens, lam, out=None, workspa
     num_pages, page_size, Hkv = kpages.shape[0], kpages.shape[1], kpages.shape[2]
     max_pages = block_table.shape[1]
     if out is None:
-        out = torch.empty((B, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 3)
     need = decode_workspace_size(B, max_pages * page_size, Hq, Hkv, D)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, max(need, 16), dtype=torch.uint8, device=q.device)
     if window is not None:
         st = LIB.diffattn_v2_decode_paged_window(_ptr(q), _ptr(kpages), _ptr(vpages), _ptr(block_table), _ptr(seqlens),
                                                  _ptr(lam), _ptr(out), B, max_pages, page_size, num_pages, Hq, Hkv, D,
@@ -525,7 +543,7 @@ def decode_f32(q, kcache, vcache, seqlens, lam, out=None, stream=None):
     B, Hq, D = q.shape
     Smax, Hkv = kcache.shape[1], kcache.shape[2]
     if out is None:
-        out = torch.empty((B, Hq // 2, D), dtype=torch.float32, device=q.device)
+        out = _empty(stream, (B, Hq // 2, D), dtype=torch.float32, device=q.device)
     _need(out, "out", torch.float32, 3)
     st = LIB.diffattn_v2_decode_f32(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(seqlens), _ptr(lam), _ptr(out), B,
                                     Smax, Hq, Hkv, D, _stream(stream, q.device))
@@ -539,7 +557,7 @@ def lambda_v1(lq1, lk1, lq2, lk2, lambda_init=0.8, rows=1, out=None, stream=None
         _need(t, n, torch.float32, 2)
     n_pairs, d = lq1.shape
     if out is None:
-        out = torch.empty((rows, n_pairs), dtype=torch.float32, device=lq1.device)
+        out = _empty(stream, (rows, n_pairs), dtype=torch.float32, device=lq1.device)
     if out.dtype != torch.float32 or not out.is_contiguous() or out.numel() != rows * n_pairs:
         raise ValueError("out must be a contiguous fp32 tensor with rows*n_pairs elements")
     st = LIB.diffattn_v2_lambda_v1(_ptr(lq1), _ptr(lk1), _ptr(lq2), _ptr(lk2), float(lambda_init), n_pairs, d, rows,
@@ -558,7 +576,7 @@ def lambda_v2(x, w_lambda, bias=None, out=None, stream=None):
     T, d = x.shape
     n_pairs = w_lambda.shape[1]
     if out is None:
-        out = torch.empty((T, n_pairs), dtype=torch.float32, device=x.device)
+        out = _empty(stream, (T, n_pairs), dtype=torch.float32, device=x.device)
     st = LIB.diffattn_v2_lambda_v2(_ptr(x), _ptr(w_lambda), _ptr(bias), T, d, n_pairs, _ptr(out),
                                    _stream(stream, x.device))
     _check(st, "diffattn_v2_lambda_v2")
@@ -580,7 +598,7 @@ def prefill_fused_lambda(q, k, v, x, w_lambda_t, bias=None, out=None, lambda_out
     Hkv = k.shape[2]
     d_model = x.shape[2]
     if out is None:
-        out = torch.empty((B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, S, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 4)
     st = LIB.diffattn_v2_prefill_fused_lambda(_ptr(q), _ptr(k), _ptr(v), _ptr(x), _ptr(w_lambda_t), _ptr(bias),
                                               _ptr(out), _ptr(lambda_out), B, S, Hq, Hkv, D, d_model,
@@ -613,7 +631,7 @@ def decode_noalloc(q, kcache, vcache, seqlens, lam, out=None, stream=None):
     B, Hq, D = q.shape
     Smax, Hkv = kcache.shape[1], kcache.shape[2]
     if out is None:
-        out = torch.empty((B, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq // 2, D), dtype=torch.bfloat16, device=q.device)
     _need(out, "out", torch.bfloat16, 3)
     st = LIB.diffattn_v2_decode_noalloc(_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(seqlens), _ptr(lam), _ptr(out),
                                         B, Smax, Hq, Hkv, D, _stream(stream, q.device))

@@ -89,6 +89,56 @@ SINK_ROPE_CACHE = {
 }
 
 
+def _lambda_v2(da, x, s, fused):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    t, w = (torch.randn(*n, generator=g, device="cuda").bfloat16() for n in ((200, 256), (256, 32)))
+    wt = w[:, :4].t().contiguous()
+    torch.cuda.synchronize()
+    if fused:
+        return lambda: da.prefill_fused_lambda(*x["qkvl"][:3], t[None], wt, stream=s)
+    return lambda: da.lambda_v2(t, w, stream=s)
+
+
+def _multi(da, x, s):
+    q, lam = x["q"][:, -2:].contiguous(), x["lam"][:, -2:].contiguous()
+    torch.cuda.synchronize()
+    return lambda: da.decode_multi(q, *x["step"][1:4], lam, stream=s)
+
+
+def _f32(da, x, s, decode):
+    y = [t.float() if t.is_floating_point() else t for t in (x["step"] if decode else x["qkvl"])]
+    torch.cuda.synchronize()
+    return (lambda: da.decode_f32(*y, stream=s)) if decode else (lambda: da.prefill_f32(*y, stream=s))
+
+
+def _lambda_v1(da, x, s):
+    y = [torch.rand(4, 64, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    return lambda: da.lambda_v1(*y, stream=s)
+
+
+PLAIN = {
+    "prefill": lambda da, x, s: lambda: da.prefill(*x["qkvl"], stream=s),
+    "prefill_window": lambda da, x, s: lambda: da.prefill_window(*x["qkvl"], 50, stream=s),
+    "prefill_varlen": lambda da, x, s: lambda: da.prefill_varlen(*x["packed"], x["cu"], 150, stream=s),
+    "prefill_varlen_window": lambda da, x, s: lambda: da.prefill_varlen_window(*x["packed"], x["cu"], 150, 50, stream=s),
+    "prefill_train": lambda da, x, s: lambda: da.prefill_train(*x["qkvl"], stream=s),
+    "prefill_varlen_train": lambda da, x, s: lambda: da.prefill_varlen_train(*x["packed"], x["cu"], 150, stream=s),
+    "backward": _backward,
+    "backward_varlen": _backward_varlen,
+    "decode": lambda da, x, s: lambda: da.decode(*x["step"], stream=s),
+    "decode_window": lambda da, x, s: lambda: da.decode(*x["step"], stream=s, window=50),
+    "decode_paged": lambda da, x, s: lambda: da.decode_paged(*x["pages"], stream=s),
+    "decode_multi": _multi,
+    "decode_noalloc": lambda da, x, s: lambda: da.decode_noalloc(*x["step"], stream=s),
+    "prefill_f32": lambda da, x, s: _f32(da, x, s, False),
+    "decode_f32": lambda da, x, s: _f32(da, x, s, True),
+    "lambda_v1": _lambda_v1,
+    "lambda_v2": lambda da, x, s: _lambda_v2(da, x, s, False),
+    "prefill_fused_lambda": lambda da, x, s: _lambda_v2(da, x, s, True),
+}
+
+
 def _tensors(out):
     return [t for t in (out if isinstance(out, (tuple, list)) else (out,)) if t is not None]
 
@@ -125,11 +175,21 @@ def test_allocations_belong_to_the_given_stream(da, x, name, raw):
     _check_pool(SINK_ROPE_CACHE[name](da, x, s.cuda_stream if raw else s), s)
 
 
-@pytest.mark.parametrize("name", ["backward", "backward_varlen"])
-def test_workspaces_belong_to_the_given_stream(da, x, name):
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", PLAIN)
+def test_allocations_of_the_other_calls_belong_to_it_too(da, x, name, raw):
+    s = torch.cuda.Stream()
+    _check_pool(PLAIN[name](da, x, s.cuda_stream if raw else s), s)
+
+
+@pytest.mark.parametrize("name,calls", [("backward", SINK_ROPE_CACHE), ("backward_varlen", SINK_ROPE_CACHE),
+                                        ("backward", PLAIN), ("backward_varlen", PLAIN), ("decode", PLAIN),
+                                        ("decode_window", PLAIN), ("decode_paged", PLAIN), ("decode_multi", PLAIN)],
+                         ids=lambda v: v if isinstance(v, str) else "plain" if v is PLAIN else "sink")
+def test_workspaces_belong_to_the_given_stream(da, x, name, calls):
     """Every allocation that the call makes, the workspace that it drops included."""
     s = torch.cuda.Stream()
-    call = SINK_ROPE_CACHE[name](da, x, s)
+    call = calls[name](da, x, s)
     torch.cuda.memory._record_memory_history(enabled="all", context=None, max_entries=10000, clear_history=True)
     try:
         out = call()
@@ -138,7 +198,7 @@ def test_workspaces_belong_to_the_given_stream(da, x, name):
     finally:
         torch.cuda.memory._record_memory_history(enabled=None)
     made = [e["stream"] for e in trace if e["action"] == "alloc"]
-    assert len(made) > len(out) and all(h == s.cuda_stream for h in made), made
+    assert len(made) > len(_tensors(out)) and all(h == s.cuda_stream for h in made), made
 
 
 def test_results_on_a_given_stream(da, x):
