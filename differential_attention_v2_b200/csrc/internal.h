@@ -44,7 +44,9 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  // (the call's own status: a failed launch takes its error with it, or the next launch would report it)
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 // With sinks, operands of the training pass that multiply keys below this (and below the number of
