@@ -6,7 +6,8 @@ current (or given) stream, and raise on a non-OK status. Output tensors and the 
 workspace are allocated with torch when the caller does not pass them.
 
 There is no CPU fallback: if the library is missing, importing fails with an error that
-says how to build it.
+says how to build it; if only the binding's native half is, the calls that go through it (with
+sinks, rotary positions, cache pages) fail with one.
 """
 from __future__ import annotations
 
@@ -15,6 +16,8 @@ import importlib.util
 import os
 
 import torch
+
+from . import build
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdiffattn_v2.so")
@@ -110,25 +113,38 @@ def _check(status: int, what: str):
 
 
 def _load_native():
-    path = os.path.join(_PKG, "_native.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing; build it with `python -m differential_attention_v2_b200.build`")
-    spec = importlib.util.spec_from_file_location(__package__ + "._native", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    """(the native half of the binding, "") or (None, why there is none): the calls that go through it
+    raise then, the others work."""
+    if not os.path.exists(build.NATIVE_PATH):
+        return None, f"{build.NATIVE_PATH} is missing"
+    if build.native_built_for() not in ("", build.native_stamp()):
+        return None, f"{build.NATIVE_PATH} was built for {build.native_built_for()}, this is {build.native_stamp()}"
+    spec = importlib.util.spec_from_file_location(__package__ + "._native", build.NATIVE_PATH)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        return None, str(e)
     module.on_error(_check)
-    return module
+    return module, ""
 
 
-_native = _load_native()
-_invoke = _native.invoke
+_native, _why_not_native = _load_native()
+
+
+def _no_native(*_):
+    raise ImportError(f"{_why_not_native}; build it with `python -m differential_attention_v2_b200.build`. "
+                      "There is no fallback implementation.")
+
+
+_invoke = _native.invoke if _native else _no_native
 
 
 def _entry(name, description):
     """An entry point of short calls: the native half checks its tensors, allocates the outputs that
     are not given and calls it on their device and the given or current stream, as described (see
     csrc/binding.cpp for the notation)."""
-    return _native.define(name, description)
+    return _native.define(name, description) if _native else None
 
 
 def _stream(stream, device):

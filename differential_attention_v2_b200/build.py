@@ -12,7 +12,9 @@ indices against the extents they address and report a violation through the devi
 word (code 4) instead of making the access. The tests load it directly.
 
 The library's Python binding has a native half, _native.so (csrc/binding.cpp, compiled with g++
-against torch's headers), which the same command builds.
+against torch's headers), which the same command builds after the library. The library itself needs
+neither torch nor Python's headers: where the native half cannot be built, a warning says so, the
+library is there, and the binding's entry points that do not go through the native half work.
 """
 from __future__ import annotations
 
@@ -23,6 +25,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,6 +34,7 @@ LIB_NAME = "libdiffattn_v2.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(PKG, "libdiffattn_v2_debug.so")
 NATIVE_PATH = os.path.join(PKG, "_native.so")
+NATIVE_STAMP_PATH = os.path.join(PKG, "_native.stamp")  # what _native.so was built for
 NATIVE_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
@@ -67,12 +71,20 @@ def nvcc() -> str:
 def build(force: bool = False, verbose: bool = False, extra_flags=None, debug_bounds: bool = False) -> str:
     """Build the library (or, with debug_bounds, its bounds-checking twin); returns its path."""
     out = DEBUG_LIB_PATH if debug_bounds else LIB_PATH
-    if not debug_bounds:
-        build_native(force=force, verbose=verbose)
     if debug_bounds:
         extra_flags = list(extra_flags or []) + ["-DDA2_DEBUG_BOUNDS"]
-    if not force and up_to_date(out):
-        return out
+    if force or not up_to_date(out):
+        _compile(out, verbose, extra_flags)
+    if not debug_bounds:
+        try:
+            build_native(force=force, verbose=verbose)
+        except (RuntimeError, ImportError, OSError) as e:
+            warnings.warn(f"{out} is built, but not the Python binding's native half, which its sink, rotary and cache "
+                          f"calls need: {e}", stacklevel=2)
+    return out
+
+
+def _compile(out, verbose, extra_flags):
     tmp = out + ".tmp"
     cmd = [nvcc()] + NVCC_FLAGS + list(extra_flags or []) + ["-I", os.path.join(ROOT, "include"), "-o", tmp] + _sources()
     if verbose:
@@ -83,13 +95,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, debug_bo
     if verbose and (res.stdout or res.stderr):
         print(res.stdout + res.stderr)
     os.replace(tmp, out)
-    return out
+
+
+def native_stamp() -> str:
+    """The interpreter and torch whose ABIs _native.so has to match."""
+    import torch
+
+    return f"python {sys.implementation.cache_tag} {sysconfig.get_config_var('SOABI')} torch {torch.__version__}"
+
+
+def native_built_for() -> str:
+    """native_stamp() of the build that made _native.so ("": there is none, or it does not say)."""
+    if not os.path.exists(NATIVE_PATH) or not os.path.exists(NATIVE_STAMP_PATH):
+        return ""
+    with open(NATIVE_STAMP_PATH) as f:
+        return f.read()
 
 
 def build_native(force: bool = False, verbose: bool = False) -> str:
-    """Build _native.so, the native half of the Python binding (g++ against torch's headers)."""
+    """Build _native.so, the native half of the Python binding (g++ against torch's headers), if a
+    source is newer or it was built for another interpreter or torch."""
     made_from = (NATIVE_SOURCE, os.path.abspath(__file__))
-    if not force and os.path.exists(NATIVE_PATH) and all(
+    stamp = native_stamp()
+    if not force and native_built_for() == stamp and all(
             os.path.getmtime(p) <= os.path.getmtime(NATIVE_PATH) for p in made_from):
         return NATIVE_PATH
     import torch
@@ -108,6 +136,8 @@ def build_native(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, NATIVE_PATH)
+    with open(NATIVE_STAMP_PATH, "w") as f:
+        f.write(stamp)
     return NATIVE_PATH
 
 
