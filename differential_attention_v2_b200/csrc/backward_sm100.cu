@@ -958,7 +958,10 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
   // Sink keys resemble one another (that is how every query finds them), so the roundings of their dS
   // add up along their common direction in dQ instead of averaging out: their blocks enter the
   // product as two bf16 terms. With bf16 alone dQ was off by 3 to 4e-3 where 1.7e-3 is its own
-  // rounding; a block more costs 16 MMAs.
+  // rounding; a block more costs 16 MMAs. That goes for however many sinks there are: with the second
+  // term for the first 512 alone, 4096 tokens, window 1024, dQ was off by 3.5e-3 where keys 512 to 639 are
+  // alike. Forward and backward of 4096 tokens, 32/8 heads, us, with it for 512 sinks and for all:
+  // 640 sinks 648 and 656, 1024 sinks 724 and 746, 2048 sinks 876 and 925.
   auto holds_sinks = [&](int t) -> bool { return kSink && 64 * key_block(t) < p.fine_keys; };
 
   const uint32_t tmem = setup(bar0, tmem_slot, abort_flag, warp);
@@ -1249,7 +1252,7 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   Params p;
   cudaError_t e;
   SinkPlan plan = {};
-  p.fine_keys = sink < kFineKeys ? sink : kFineKeys;
+  p.fine_keys = sink;  // (also where the mask is the causal one: the sinks are keys like any other then)
   if (o_branch_f32) {
     // the sink form; window <= 0: every earlier key, the causal mask
     if (window <= 0) {

@@ -49,10 +49,6 @@ cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t s
   return e;
 }
 
-// With sinks, operands of the training pass that multiply keys below this (and below the number of
-// sinks) are kept as two bf16 terms.
-constexpr int kFineKeys = 512;
-
 // bf16 prefill on tcgen05 (D = 128); window > 0 (causal only) limits query i to keys
 // i-window+1 .. i. With cu_seqlens (device, B+1 entries) the tensors hold B packed sequences
 // as one [1,T] batch and S is the longest sequence. Tensor maps: Q over [B,S,Hq,D], K/V over [B,S,Hkv,D],

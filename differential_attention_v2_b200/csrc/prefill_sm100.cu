@@ -1120,7 +1120,7 @@ cudaError_t launch_prefill(const CUtensorMap& tmQ, const CUtensorMap& tmK, const
   using namespace prefill;
   Params p;
   p.sink = window > 0 ? sink : 0;
-  p.fine_keys = sink < kFineKeys ? sink : kFineKeys;
+  p.fine_keys = sink;
   p.o_branch_f32 = o_branch_f32;
   p.lambda = lambda;
   p.out = out;

@@ -481,7 +481,7 @@ DA2_API int diffattn_v2_prefill_varlen_window_sink(const void* q, const void* k,
  * those of diffattn_v2_prefill_window_train / diffattn_v2_backward_window (and the packed forms),
  * but o_branch is FP32 [B,S,Hq,D] ([T,Hq,D]): sinks draw most of a row's weight to one key, where
  * dS = A (dO.v_j - dO.O_b) is a small difference of large terms that a bf16 O_b would drown. For the
- * same reason the products over (the first 512) sink keys keep their weights and dS as two bf16 terms,
+ * same reason the products over sink keys keep their weights and dS as two bf16 terms,
  * so that `out` here is nearer the exact value than the inference call's, not bit for bit the same. A
  * sequence's first query sees a single key, so its softmax is constant: its dq, and its part of dk, are
  * exactly 0. Packed sequences each launch the longest one's tiles: DA2_ERR_UNSUPPORTED where
