@@ -77,6 +77,7 @@ int diffattn_v2_rope(const void* q, const void* k, void* q_out, void* k_out, con
     p.k_stride = k_stride;
     p.ko_stride = k_out_stride;
   }
+  if (da2::bounds_error_word(&p.err) != cudaSuccess) return DA2_ERR_CUDA;
   return status_of(da2::launch_rope(p, dtype == DA2_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -115,6 +116,7 @@ int diffattn_v2_rope_append_paged(const void* q, const void* k, const void* v, v
   p.B = B;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
+  if (da2::bounds_error_word(&p.err) != cudaSuccess) return DA2_ERR_CUDA;
   return status_of(da2::launch_rope(p, dtype == DA2_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -106,6 +106,7 @@ struct Params {
   int sink_tiles, sink_parts, tile_parts, part_steps;
   float* partial;
   const int* slot_off;
+  size_t stat_floats, slots;  // debug-bounds build: extents of stats and partial
 };
 
 // With sinks the dK/dV work of a KV head is uneven: a tile that holds sinks is seen by every later
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(256, 4)
 preprocess_sink_kernel(const __nv_bfloat16* dout, const float* o_branch,
                        const float* lse, const float* lambda, float* stats,
                        float* dlam, const int* cu, const int* pad_off, int B,
-                       int S, int S_pad, int n_pairs) {
+                       int S, int S_pad, int n_pairs, size_t rows, size_t stat_floats, int* err) {
   pdl_wait();
   __shared__ float rec[kStatArrays * kStatBlock];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -340,7 +341,7 @@ preprocess_sink_kernel(const __nv_bfloat16* dout, const float* o_branch,
   float term = 0.f;
   {
     const int r = lane < 16 ? lane >> 1 : lane & 7, i = i0 + 8 * warp + r;
-    if (i < n) {
+    if (i < n && checked(base + i < rows, err)) {
       const size_t at = (base + i) * n_pairs + pair;
       if (lane < 16) term = lse[at * 2 + (lane & 1)];
       else if (lane < 24) term = lambda[at];
@@ -358,7 +359,7 @@ preprocess_sink_kernel(const __nv_bfloat16* dout, const float* o_branch,
       const int i = i0 + 8 * warp + r0 + u;
       g[u] = make_uint2(0u, 0u);
       o[u][0] = o[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n) {
+      if (i < n && checked(base + i < rows, err)) {
         const size_t at = (base + i) * n_pairs + pair;
         g[u] = __ldcs(reinterpret_cast<const uint2*>(dout + at * HD) + lane);
         const float4* ob = reinterpret_cast<const float4*>(o_branch + at * 2 * HD);
@@ -389,10 +390,12 @@ preprocess_sink_kernel(const __nv_bfloat16* dout, const float* o_branch,
     rec[2 * kStatBlock + 8 * warp + lane] = -e1;
     rec[3 * kStatBlock + 8 * warp + lane] = -e2;
     const int i = i0 + 8 * warp + lane;
-    if (i < n) dlam[(base + i) * n_pairs + pair] = -e2;
+    if (i < n && checked(base + i < rows, err)) dlam[(base + i) * n_pairs + pair] = -e2;
   }
   __syncthreads();
-  float* dst = stats + stat_index(kVarlen ? pair : bp, S_pad, blk * kStatBlock, 0);
+  const size_t to = stat_index(kVarlen ? pair : bp, S_pad, blk * kStatBlock, 0);
+  if (!checked(to + kStatArrays * kStatBlock <= stat_floats, err)) return;
+  float* dst = stats + to;
   for (int i = threadIdx.x; i < kStatArrays * kStatBlock; i += 256) dst[i] = rec[i];
 }
 
@@ -676,8 +679,9 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmQ, const CUtensorM
           tma_load_4d(st + kStreamTile + c * kStreamChunk, &tmQ, bar(kXFull + s), c * 64, 2 * pair + 1, tok0 + q0, tb);
           tma_load_4d(st + 2 * kStreamTile + c * kStreamChunk, &tmO, bar(kXFull + s), c * 64, pair, tok0 + q0, tb);
         }
-        bulk_load(st + 3 * kStreamTile, p.stats + stat_index(sb + pair, p.S_pad, srow0 + q0, 0),
-                  kStatBytes, bar(kXFull + s));
+        const size_t stat = stat_index(sb + pair, p.S_pad, srow0 + q0, 0);
+        if (checked(stat + kStatArrays * kStatBlock <= p.stat_floats, p.err))
+          bulk_load(st + 3 * kStreamTile, p.stats + stat, kStatBytes, bar(kXFull + s));
         issued = t + 1;
       }
       if (*abort_flag) {
@@ -852,9 +856,11 @@ __device__ __forceinline__ void dkdv_cta(const CUtensorMap& tmQ, const CUtensorM
       const size_t total_rows = kVarlen ? static_cast<size_t>(ld_in<kSink>(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
       const bool valid = key < S && checked(off + 128 / kGroups <= total_rows * p.Hkv * HD, p.err);
       if (kSink && parts > 1) {
-        float* dst = p.partial + partial_slot<kVarlen>(p, b, g, tile, part, parts) * kSlotFloats + r * HD + d0;
-        store_row_f32(trow + kTmAcc0 + d0, dst, 1.f);
-        store_row_f32(trow + kTmAcc1 + d0, dst + kSlotFloats / 2, p.scale);
+        const size_t slot = partial_slot<kVarlen>(p, b, g, tile, part, parts);
+        const bool fits = checked(slot < p.slots, p.err);  // (uniform over the CTA)
+        float* dst = p.partial + slot * kSlotFloats + r * HD + d0;
+        if (fits) store_row_f32(trow + kTmAcc0 + d0, dst, 1.f);
+        if (fits) store_row_f32(trow + kTmAcc1 + d0, dst + kSlotFloats / 2, p.scale);
       } else {
         store_row(trow + kTmAcc0 + d0, p.dv + off, 1.f, valid);
         store_row(trow + kTmAcc1 + d0, p.dk + off, p.scale, valid);
@@ -894,7 +900,9 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const Params p) 
   const int parts = parts_of((q_end - q_first) * (p.Hq / p.Hkv / 2), tile < p.sink_tiles ? p.sink_parts : p.tile_parts,
                              p.part_steps);
   if (parts == 1) return;
-  const float* src = p.partial + partial_slot<kVarlen>(p, b, g, tile, 0, parts) * kSlotFloats;
+  const size_t slot = partial_slot<kVarlen>(p, b, g, tile, 0, parts);
+  if (!checked(slot + parts <= p.slots, p.err)) return;
+  const float* src = p.partial + slot * kSlotFloats;
 #pragma unroll
   for (int i = 0; i < 2 * 16 * HD / 4 / kSumThreads; ++i) {
     const int u = i * kSumThreads + threadIdx.x;  // which of dV, dK; row; float4 of the row
@@ -909,7 +917,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const Params p) 
       a.z += v.z;
       a.w += v.w;
     }
-    if (r0 + row < S)
+    const size_t rows = kVarlen ? static_cast<size_t>(*(p.cu_seqlens + p.B)) : static_cast<size_t>(p.B) * p.S;
+    if (r0 + row < S && checked(row_base + r0 + row < rows, p.err))
       *reinterpret_cast<uint2*>((which ? p.dk : p.dv) + ((row_base + r0 + row) * p.Hkv + g) * HD + 4 * c) =
           make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
   }
@@ -1085,11 +1094,12 @@ __device__ __forceinline__ void dq_cta(const CUtensorMap& tmQ, const CUtensorMap
     const int sr = srow0 + qi;  // this row in the row terms (past the sequence: -lse = -inf)
     // (with sinks query 0 too: it sees one key, so its dS is 0 and dP - E is only rounding)
     const bool lone = kSink && qi == 0;
-    const float nl1 = lone ? -INFINITY : ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 0));
-    const float nl2 = lone ? -INFINITY : ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 1));
-    const uint64_t ne1 = f2_pack(ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 2)), ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 2)));
-    const uint64_t ne2 = f2_pack(ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 3)), ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 3)));
-    const float nlam_s = ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, 4));
+    const bool stat_ok = checked(stat_index(bp, p.S_pad, sr, kStatArrays - 1) < p.stat_floats, p.err);
+    auto term = [&](int k) -> float { return stat_ok ? ld_in<kSink>(p.stats + stat_index(bp, p.S_pad, sr, k)) : 0.f; };
+    const float nl1 = lone ? -INFINITY : term(0);
+    const float nl2 = lone ? -INFINITY : term(1);
+    const float e1 = term(2), e2 = term(3), nlam_s = term(4);
+    const uint64_t ne1 = f2_pack(e1, e1), ne2 = f2_pack(e2, e2);
     const uint64_t nl1_2 = f2_pack(nl1, nl1), nl2_2 = f2_pack(nl2, nl2), nlam = f2_pack(nlam_s, nlam_s);
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     for (int t = 0; ok && t < n_steps; ++t) {
@@ -1265,7 +1275,8 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   if (cu_seqlens) {
     // S is the longest sequence; the row terms of all sequences form one padded batch
     const int S_pad = static_cast<int>(varlen_stat_rows(B, total_tokens));
-    int* pad_off = reinterpret_cast<int*>(workspace + static_cast<size_t>(n_pairs) * S_pad * kStatArrays);
+    p.stat_floats = static_cast<size_t>(n_pairs) * S_pad * kStatArrays;
+    int* pad_off = reinterpret_cast<int*>(workspace + p.stat_floats);
     if (o_branch_f32) {
       int* slot_off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(workspace) +
                                              backward_varlen_workspace_bytes(B, total_tokens, Hq));
@@ -1282,7 +1293,7 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     if (o_branch_f32) {
       e = launch_chained(preprocess_sink_kernel<true>, dim3(static_cast<unsigned>(warps / kStatBlock)), dim3(256), 0, 0,
                          stream, dout, o_branch_f32, lse, lambda, workspace, dlambda, cu_seqlens, pad_off, B, S, S_pad,
-                         n_pairs);
+                         n_pairs, static_cast<size_t>(total_tokens), p.stat_floats, err);
       if (e != cudaSuccess) return e;
     } else
       preprocess_varlen_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
@@ -1292,10 +1303,11 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
   } else {
     const int S_pad = (S + kRowPad - 1) / kRowPad * kRowPad;
     const long long warps = static_cast<long long>(B) * S_pad * n_pairs;
+    p.stat_floats = static_cast<size_t>(warps) * kStatArrays;
     if (o_branch_f32) {
       e = launch_chained(preprocess_sink_kernel<false>, dim3(static_cast<unsigned>(warps / kStatBlock)), dim3(256), 0, 0,
                          stream, dout, o_branch_f32, lse, lambda, workspace, dlambda, nullptr, nullptr, B, S, S_pad,
-                         n_pairs);
+                         n_pairs, static_cast<size_t>(B) * S, p.stat_floats, err);
       if (e != cudaSuccess) return e;
     } else
       preprocess_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(
@@ -1337,6 +1349,7 @@ cudaError_t launch_backward_sm100(const CUtensorMap& tmQ64, const CUtensorMap& t
     p.sink_parts = plan.sink_parts;
     p.tile_parts = plan.tile_parts;
     p.part_steps = plan.part_steps;
+    p.slots = static_cast<size_t>(plan.slots);
     p.partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
                                          sink_slots_offset(B, S, total_tokens, Hq, cu_seqlens != nullptr));
     const int tile_ctas = plan.sink_tiles * plan.sink_parts + (p.n_tiles - plan.sink_tiles) * plan.tile_parts;

@@ -157,11 +157,12 @@ __device__ __forceinline__ int pages_of(int len, int shift) { return (max(len, 0
 // ---------------------------------------------------------------------------------- extend
 __global__ void __launch_bounds__(kThreads)
 extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_new, int32_t* result, int B,
-              int max_pages, int shift, int num_pages) {
+              int max_pages, int shift, int num_pages, int* err) {
   pdl_wait();
   cluster_arrive_relaxed();
   __shared__ Shared sh;
   __shared__ int pre[kMaxCacheSeqs], first[kMaxCacheSeqs];
+  if (!checked(B > 0 && B <= kMaxCacheSeqs, err)) return;  // (the whole cluster)
   cg::cluster_group cl = cg::this_cluster();
   const int lane = threadIdx.x & 31, gw = static_cast<int>(cl.block_rank()) * kWarps + (threadIdx.x >> 5);
   if (threadIdx.x == 0) sh.flag = 0;
@@ -189,6 +190,7 @@ extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_
     take_free(refs, lo, hi, base, want, lane, [&](int r, int p) {
       const int b = owner_of(pre, B, r);
       const int at = first[b] + r - (b > 0 ? pre[b - 1] : 0);
+      if (!checked(at >= 0 && at < max_pages && p < num_pages, err)) return;
       table[static_cast<size_t>(b) * max_pages + at] = p;
       refs[p] = 1;
     });
@@ -201,11 +203,12 @@ extend_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_
 // ------------------------------------------------------------------------------------ fork
 __global__ void __launch_bounds__(kThreads)
 fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* parents, const int32_t* children,
-            int2* copies, int32_t* result, int n, int B, int max_pages, int shift, int num_pages) {
+            int2* copies, int32_t* result, int n, int B, int max_pages, int shift, int num_pages, int* err) {
   pdl_wait();
   cluster_arrive_relaxed();
   __shared__ Shared sh;
   __shared__ int pre[kMaxCacheSeqs], kid[kMaxCacheSeqs], len[kMaxCacheSeqs];
+  if (!checked(n > 0 && n <= kMaxCacheSeqs, err)) return;  // (the whole cluster)
   cg::cluster_group cl = cg::this_cluster();
   const int rank = static_cast<int>(cl.block_rank());
   const int lane = threadIdx.x & 31, gw = rank * kWarps + (threadIdx.x >> 5);
@@ -244,6 +247,7 @@ fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* pare
     take_free(refs, lo, hi, base, want, lane, [&](int r, int p) {
       const int i = owner_of(pre, n, r);
       const int at = len[i] >> shift;
+      if (!checked(i < n && at < max_pages && p < num_pages && parents[i] < B && kid[i] >= 0 && kid[i] < B, err)) return;
       const int src = table[static_cast<size_t>(parents[i]) * max_pages + at];
       copies[i] = src >= 0 && src < num_pages ? make_int2(src, p) : make_int2(-1, -1);
       table[static_cast<size_t>(kid[i]) * max_pages + at] = p;
@@ -260,7 +264,7 @@ fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* pare
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int l = l0 + 32 * u + lane;
-        if (l < whole) {
+        if (l < whole && checked(l < max_pages, err)) {
           const int e = from[l];
           to[l] = e;
           if (e >= 0 && e < num_pages) atomicAdd(refs + e, 1);
@@ -279,7 +283,7 @@ fork_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* pare
 // ------------------------------------------------------------------------------------ trim
 __global__ void __launch_bounds__(kThreads)
 trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B, int max_pages, int shift,
-            int num_pages, int window, int keep) {
+            int num_pages, int window, int keep, int* err) {
   pdl_wait();
   cluster_arrive_relaxed();
   __shared__ Shared sh;
@@ -298,7 +302,7 @@ trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* resu
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int l = l0 + 32 * u + lane;
-      if (l >= keep && l < end) {
+      if (l >= keep && l < end && checked(b < B && l >= 0 && l < max_pages, err)) {
         const int e = row[l];
         if (e >= 0) {
           row[l] = -1;
@@ -316,7 +320,7 @@ trim_kernel(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* resu
 // ------------------------------------------------------------------------------------ free
 __global__ void __launch_bounds__(kThreads)
 free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result, int n, int B,
-            int max_pages, int num_pages) {
+            int max_pages, int num_pages, int* err) {
   pdl_wait();
   cluster_arrive_relaxed();
   __shared__ Shared sh;
@@ -335,6 +339,7 @@ free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs
     for (long long it = gw; it < static_cast<long long>(n) * per; it += kAllWarps) {
       const int b = seqs[it / per], l0 = static_cast<int>(it % per) * 128;
       if (b < 0) continue;  // padding
+      if (!checked(b < B, err)) continue;
       int32_t* row = table + static_cast<size_t>(b) * max_pages;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -355,7 +360,7 @@ free_kernel(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs
 // n live pages; the r-th live page at or behind n goes to the r-th free one before it.
 __global__ void __launch_bounds__(kThreads)
 compact_kernel(const int32_t* table, const int32_t* refs, int32_t* table_out, int32_t* refs_out, int2* moves,
-               int32_t* result, int B, int max_pages, int num_pages) {
+               int32_t* result, int B, int max_pages, int num_pages, int* err) {
   pdl_wait();
   cluster_arrive_relaxed();
   __shared__ Shared sh;
@@ -380,8 +385,8 @@ compact_kernel(const int32_t* table, const int32_t* refs, int32_t* table_out, in
     const unsigned m = __ballot_sync(0xffffffffu, live);
     const int lr = r_live + __popc(m & ((1u << lane) - 1u));  // live pages before p
     if (p < hi) {
-      if (live && p >= n) mv[lr - before].x = p;
-      if (!live && p < n) mv[p - lr].y = p;
+      const int at = live ? lr - before : p - lr;
+      if (live != (p < n) && checked(at >= 0 && at < num_pages / 2, err)) (live ? mv[at].x : mv[at].y) = p;
     }
     r_live += __popc(m);
   }
@@ -395,6 +400,7 @@ compact_kernel(const int32_t* table, const int32_t* refs, int32_t* table_out, in
   }
   for (int r = gt; r < n_moves; r += kAllThreads) {
     const int2 m = __ldcg(mv + r);
+    if (!checked(m.x >= 0 && m.x < num_pages && m.y >= 0 && m.y < num_pages, err)) continue;
     const int c = refs[m.x];
     refs_out[m.y] = c;
     refs_out[m.x] = 0;
@@ -426,7 +432,7 @@ constexpr int kPieceVecs = kCopyThreads * kCopyUnroll;
 
 __global__ void __launch_bounds__(kCopyThreads)
 copy_kernel(uint4* k, uint4* v, const int2* copies, int n, int num_pages,
-            int page_vecs, int pieces) {
+            int page_vecs, int pieces, int* err) {
   pdl_wait();
   const long long items = static_cast<long long>(n) * 2 * pieces;
   long long it = blockIdx.x;
@@ -440,6 +446,7 @@ copy_kernel(uint4* k, uint4* v, const int2* copies, int n, int num_pages,
     const uint4* src = pool + static_cast<size_t>(c.x) * page_vecs;
     uint4* dst = pool + static_cast<size_t>(c.y) * page_vecs;
     const int at = static_cast<int>(it % pieces) * kPieceVecs + threadIdx.x;
+    if (!checked(it / pieces / 2 < n && at >= 0, err)) continue;
     uint4 x[kCopyUnroll];
 #pragma unroll
     for (int i = 0; i < kCopyUnroll; ++i)
@@ -455,38 +462,48 @@ copy_kernel(uint4* k, uint4* v, const int2* copies, int n, int num_pages,
 cudaError_t launch_cache_extend(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* n_new,
                                 int32_t* result, int B, int max_pages, int page_shift, int num_pages,
                                 cudaStream_t stream) {
+  int* err = nullptr;
+  if (const cudaError_t e = bounds_error_word(&err); e != cudaSuccess) return e;
   return launch_chained(pages::extend_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
-                        table, seqlens, refs, n_new, result, B, max_pages, page_shift, num_pages);
+                        table, seqlens, refs, n_new, result, B, max_pages, page_shift, num_pages, err);
 }
 
 cudaError_t launch_cache_fork(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* parents,
                               const int32_t* children, int32_t* copies, int32_t* result, int n, int B, int max_pages,
                               int page_shift, int num_pages, cudaStream_t stream) {
+  int* err = nullptr;
+  if (const cudaError_t e = bounds_error_word(&err); e != cudaSuccess) return e;
   return launch_chained(pages::fork_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
                         table, seqlens, refs, parents, children, reinterpret_cast<int2*>(copies), result, n, B,
-                        max_pages, page_shift, num_pages);
+                        max_pages, page_shift, num_pages, err);
 }
 
 cudaError_t launch_cache_trim(int32_t* table, const int32_t* seqlens, int32_t* refs, int32_t* result, int B,
                               int max_pages, int page_shift, int num_pages, int window, int sink,
                               cudaStream_t stream) {
+  int* err = nullptr;
+  if (const cudaError_t e = bounds_error_word(&err); e != cudaSuccess) return e;
   const int keep = static_cast<int>((static_cast<long long>(sink) + (1 << page_shift) - 1) >> page_shift);
   return launch_chained(pages::trim_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
-                        table, seqlens, refs, result, B, max_pages, page_shift, num_pages, window, keep);
+                        table, seqlens, refs, result, B, max_pages, page_shift, num_pages, window, keep, err);
 }
 
 cudaError_t launch_cache_free(int32_t* table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result,
                               int n, int B, int max_pages, int num_pages, cudaStream_t stream) {
+  int* err = nullptr;
+  if (const cudaError_t e = bounds_error_word(&err); e != cudaSuccess) return e;
   return launch_chained(pages::free_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
-                        table, seqlens, refs, seqs, result, n, B, max_pages, num_pages);
+                        table, seqlens, refs, seqs, result, n, B, max_pages, num_pages, err);
 }
 
 cudaError_t launch_cache_compact(const int32_t* table, const int32_t* refs, int32_t* table_out, int32_t* refs_out,
                                  int32_t* moves, int32_t* result, int B, int max_pages, int num_pages,
                                  cudaStream_t stream) {
+  int* err = nullptr;
+  if (const cudaError_t e = bounds_error_word(&err); e != cudaSuccess) return e;
   return launch_chained(pages::compact_kernel, dim3(pages::kCtas), dim3(pages::kThreads), 0, pages::kCtas, stream,
                         table, refs, table_out, refs_out, reinterpret_cast<int2*>(moves), result, B, max_pages,
-                        num_pages);
+                        num_pages, err);
 }
 
 cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int n, int num_pages, size_t page_bytes,
@@ -494,7 +511,10 @@ cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int
   const int page_vecs = static_cast<int>(page_bytes / 16);
   const int pieces = (page_vecs + pages::kPieceVecs - 1) / pages::kPieceVecs;
   int device = 0, n_sms = 0;
-  cudaError_t e = cudaGetDevice(&device);
+  int* err = nullptr;
+  cudaError_t e = bounds_error_word(&err);
+  if (e != cudaSuccess) return e;
+  e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&n_sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return e;
@@ -504,7 +524,7 @@ cudaError_t launch_cache_copy_pages(void* k, void* v, const int32_t* copies, int
   const long long most = 64LL * n_sms;
   return launch_chained(pages::copy_kernel, dim3(static_cast<unsigned>(items < most ? items : most)),
                         dim3(pages::kCopyThreads), 0, 0, stream, static_cast<uint4*>(k), static_cast<uint4*>(v),
-                        reinterpret_cast<const int2*>(copies), n, num_pages, page_vecs, pieces);
+                        reinterpret_cast<const int2*>(copies), n, num_pages, page_vecs, pieces, err);
 }
 
 }  // namespace da2

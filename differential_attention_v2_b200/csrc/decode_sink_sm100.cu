@@ -150,7 +150,7 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
     const int t = chunk_tok(k), lp = t >> p.page_shift;
     const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
     if (checked(lp < p.max_pages, p.err)) entry0 = *(row + lp);
-    if (small_pages && t + 8 < n) entry1 = *(row + lp + 1);
+    if (small_pages && t + 8 < n && checked(lp + 1 < p.max_pages, p.err)) entry1 = *(row + lp + 1);
   };
   // chunk k into its slot (the whole warp calls; lane 0 copies)
   auto issue = [&](int k) {

@@ -177,11 +177,21 @@ struct RopeParams {
   int n_axes, P, T, Hq, Hkv, D, inverse, interleaved;
   const int32_t *block_table, *seqlens, *cu_seqlens;
   int B, max_pages, page_shift, num_pages;
+  int* err;  // debug-bounds build: the device error word
 };
 cudaError_t launch_rope(const RopeParams& p, bool f32, cudaStream_t stream);
 
 // Address of the device error word on the current device.
 cudaError_t device_error_word(int** out);
+// The same for kernels that report violated bounds and nothing else (null in the normal build).
+inline cudaError_t bounds_error_word(int** out) {
+#ifdef DA2_DEBUG_BOUNDS
+  return device_error_word(out);
+#else
+  *out = nullptr;
+  return cudaSuccess;
+#endif
+}
 
 // 4-D bf16 tensor map over a row-major [B,S,H,D] array, box {box0, 1, box2, 1}, 128-byte swizzle.
 cudaError_t encode_bshd_bf16(CUtensorMap* map, const void* base, uint64_t D, uint64_t H, uint64_t S, uint64_t B,

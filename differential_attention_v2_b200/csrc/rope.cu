@@ -24,6 +24,7 @@
 // Append: k goes to the row of its page (token i of sequence b's n_b new ones is logical position
 // seqlens[b] - n_b + i) and v beside it, so that neither is written to a buffer in between.
 
+#include "bounds.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -89,6 +90,7 @@ __device__ __forceinline__ long long cache_row(const RopeParams& p, int t, int l
   }
   const int at = *(p.seqlens + b) - (end - t);
   if (at < 0 || (at >> p.page_shift) >= p.max_pages) return -1;
+  if (!checked(b < p.B, p.err)) return -1;
   const int page = *(p.block_table + static_cast<size_t>(b) * p.max_pages + (at >> p.page_shift));
   if (page < 0 || page >= p.num_pages) return -1;
   return (static_cast<long long>(page) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
@@ -96,12 +98,13 @@ __device__ __forceinline__ long long cache_row(const RopeParams& p, int t, int l
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Heads h, h + step, .. < n of one tensor at element offsets off + h * D: turned, or copied.
+// Heads h, h + step, .. < n of one tensor (of `heads`) at element offsets off + h * D: turned, or copied.
 template <typename T, int N, bool kInter, bool kTurn>
-__device__ __forceinline__ void walk(const T* src, T* dst, int h, int step, int n, int D,
-                                     int ra, int rb, const float (&co)[N], const float (&si)[N]) {
+__device__ __forceinline__ void walk(const T* src, T* dst, int h, int step, int n, int heads, int D,
+                                     int ra, int rb, const float (&co)[N], const float (&si)[N], int* err) {
   using V = Vec<T, N>;
   for (; h < n; h += step) {
+    if (!checked(h >= 0 && h < heads && ra + N <= D && rb + N <= D, err)) continue;
     V x = *reinterpret_cast<const V*>(src + h * D + ra);
     V y = *reinterpret_cast<const V*>(src + h * D + rb);
     if constexpr (kTurn) {
@@ -165,7 +168,7 @@ rope_kernel(const RopeParams p, const int chunks, const int chunk_heads) {
     for (int j = 0; j * hpw < N; ++j) {
       const int e0 = j * hpw + hs, c = r * N + e0;
       float s = 0.f, k = 1.f;
-      if (rot && e0 < N) {
+      if (rot && e0 < N && checked(c < p.P, p.err)) {
         int axis = 0;
         while (axis + 1 < p.n_axes && c >= p.sec_end[axis]) ++axis;
         double turn = static_cast<double>(*(p.positions + static_cast<size_t>(axis) * p.T + t)) *
@@ -191,21 +194,21 @@ rope_kernel(const RopeParams p, const int chunks, const int chunk_heads) {
     const int nq = min(h1, p.Hq);
     int h = h0 + hs;
     // a unit that passes through has cos 1 and sin 0, but is copied: -0 and NaN keep their bits
-    if (rot) walk<T, N, kInter, true>(q, qo, h, hpw, nq, p.D, ra, rb, co, si);
-    else walk<T, N, kInter, false>(q, qo, h, hpw, nq, p.D, ra, rb, co, si);
+    if (rot) walk<T, N, kInter, true>(q, qo, h, hpw, nq, p.Hq, p.D, ra, rb, co, si, p.err);
+    else walk<T, N, kInter, false>(q, qo, h, hpw, nq, p.Hq, p.D, ra, rb, co, si, p.err);
     if (h < p.Hq) h += (p.Hq - h + hpw - 1) / hpw * hpw;
     if (h >= h1 || (kAppend && row < 0)) continue;  // (no page for this token: only its q is written)
     const size_t at = kAppend ? static_cast<size_t>(row) * p.Hkv * p.D : tt * p.ko_stride;
     const T* k = static_cast<const T*>(p.k) + tt * p.k_stride;
     T* ko = static_cast<T*>(p.k_out) + at;
     const int nk = min(h1 - p.Hq, p.Hkv);
-    if (rot) walk<T, N, kInter, true>(k, ko, h - p.Hq, hpw, nk, p.D, ra, rb, co, si);
-    else walk<T, N, kInter, false>(k, ko, h - p.Hq, hpw, nk, p.D, ra, rb, co, si);
+    if (rot) walk<T, N, kInter, true>(k, ko, h - p.Hq, hpw, nk, p.Hkv, p.D, ra, rb, co, si, p.err);
+    else walk<T, N, kInter, false>(k, ko, h - p.Hq, hpw, nk, p.Hkv, p.D, ra, rb, co, si, p.err);
     if (kAppend) {
       h -= p.Hq + p.Hkv;
       if (h < 0) h += (-h + hpw - 1) / hpw * hpw;
       walk<T, N, kInter, false>(static_cast<const T*>(p.v) + tt * p.v_stride, static_cast<T*>(p.v_out) + at, h, hpw,
-                                h1 - p.Hq - p.Hkv, p.D, ca, cb, co, si);
+                                h1 - p.Hq - p.Hkv, p.Hkv, p.D, ca, cb, co, si, p.err);
     }
   }
 }
