@@ -54,6 +54,17 @@ cudaError_t get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   return cudaSuccess;
 }
 
+// The encoder is a driver function, and fails on a host thread that has no context yet; the runtime's
+// own calls make the device's context current as they need it. So a failure is tried again with it.
+template <typename... A>
+CUresult encode_tiled(PFN_cuTensorMapEncodeTiled_v12000 enc, A... args) {
+  CUresult r = enc(args...);
+  if (r == CUDA_SUCCESS) return r;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+  return enc(args...);
+}
+
 // 4-D bf16 tensor map over a [d3, d2, d1, d0] row-major array (d0 = D innermost), box
 // {box0, 1, box2, 1}, 128-byte swizzle, out-of-range elements read as zero.
 cudaError_t encode_bshd(CUtensorMap* map, const void* base, uint64_t D, uint64_t H, uint64_t S, uint64_t B,
@@ -65,7 +76,7 @@ cudaError_t encode_bshd(CUtensorMap* map, const void* base, uint64_t D, uint64_t
   const cuuint64_t strides[3] = {D * 2, H * D * 2, S * H * D * 2};  // bytes, dims 1..3
   const cuuint32_t box[4] = {box0, 1, box2, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = encode_tiled(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -132,7 +143,7 @@ cudaError_t encode_2d_bf16(CUtensorMap* map, const void* base, uint64_t cols, ui
   const cuuint64_t strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = encode_tiled(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -146,7 +157,7 @@ cudaError_t encode_kv_halves(CUtensorMap* map, const void* base, uint64_t H, uin
   const cuuint64_t strides[4] = {H * 256, 128, 256, S * H * 256};  // bytes, dims 1..4
   const cuuint32_t box[5] = {64, tokens, 2, 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = encode_tiled(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -160,7 +171,7 @@ cudaError_t encode_out_bf16(CUtensorMap* map, void* base, uint64_t D, uint64_t H
   const cuuint64_t strides[3] = {D * 2, H * D * 2, S * H * D * 2};
   const cuuint32_t box[4] = {32, 1, 32, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  CUresult r = encode_tiled(enc, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

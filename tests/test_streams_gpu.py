@@ -254,3 +254,32 @@ def test_a_refused_result_keeps_its_value(da, name):
     if name != "trim":  # (takes no list)
         with pytest.raises(TypeError):
             call(da, pool, [])
+
+
+ALL = {**{f"sink {n}": c for n, c in SINK_ROPE_CACHE.items()}, **{f"plain {n}": c for n, c in PLAIN.items()}}
+
+
+@pytest.mark.parametrize("name", ALL)
+def test_the_first_call_of_a_host_thread(da, x, name):
+    """A thread that has made no CUDA call yet, as a server's worker. (All that the call allocates is cached by
+    then, so that not even the allocator calls the runtime before it.)"""
+    import threading
+
+    call = ALL[name](da, x, None)
+    ref = _tensors(call())
+    torch.cuda.synchronize()
+    ref = [t.clone() for t in ref]
+    got = []
+
+    def work():
+        try:
+            got.append(_tensors(call()))
+        except Exception as e:  # noqa: BLE001
+            got.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not isinstance(got[0], Exception), got[0]
+    assert all(torch.equal(a, b) for a, b in zip(got[0], ref))
