@@ -699,8 +699,6 @@ def cache_fork(block_table, seqlens, refs, parents, children, page_size, copies=
     """Row children[i] (empty) continues what row parents[i] holds: whole pages are shared, a partly
     filled last page gets a page of its own. Returns (copies int32 [n,2] for cache_copy_pages, -1
     where there is none; result int32 [1]: pages taken, -1 too few free pages, -2 a bad pair)."""
-    if block_table.shape[0] == 0 and parents.numel() > 0:
-        raise ValueError("parents: the table has no rows")
     copies, result = _invoke(_CACHE_FORK, LIB.addresses["diffattn_v2_cache_fork"], block_table, seqlens, refs, parents,
                              children, page_size, copies, result, stream)
     return copies, _of_nothing(result, parents.numel() == 0, stream)
@@ -718,7 +716,7 @@ def cache_free(block_table, seqlens, refs, seqs, result=None, stream=None):
     """The listed sequences (int32; negative entries are padding) give their pages back and become
     empty. Returns result int32 [1]: pages that became free, or -2 (an index >= B; nothing changed)."""
     result = _invoke(_CACHE_FREE, LIB.addresses["diffattn_v2_cache_free"], block_table, seqlens, refs, seqs, result, stream)
-    return _of_nothing(result, seqs.numel() == 0 or seqlens.numel() == 0, stream)
+    return _of_nothing(result, seqs.numel() == 0, stream)
 
 
 def cache_compact(block_table, refs, block_table_out=None, refs_out=None, moves=None, result=None, stream=None):

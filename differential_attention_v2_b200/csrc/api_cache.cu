@@ -138,9 +138,9 @@ int diffattn_v2_cache_fork(int32_t* block_table, int32_t* seqlens, int32_t* refs
                            int page_size, int num_pages, da2_stream_t stream) {
   const int shift = da2::page_shift_of(page_size);
   if (n < 0 || !pool_ok(B, max_pages, shift, num_pages)) return DA2_ERR_INVALID;
-  if (n == 0 || B == 0) return DA2_OK;
-  if (!ints_ok(block_table, seqlens, refs, parents, children, result) || !copies || !da2::is_aligned(copies, 8))
-    return DA2_ERR_INVALID;
+  if (n == 0) return DA2_OK;
+  if (!ints_ok(refs, parents, children, result) || !copies || !da2::is_aligned(copies, 8)) return DA2_ERR_INVALID;
+  if (B > 0 && !ints_ok(block_table, seqlens)) return DA2_ERR_INVALID;  // (a table without rows is not read)
   if (n > da2::kMaxCacheSeqs) return DA2_ERR_UNSUPPORTED;
   return status_of(da2::launch_cache_fork(block_table, seqlens, refs, parents, children, copies, result, n, B, max_pages,
                                           shift, num_pages, reinterpret_cast<cudaStream_t>(stream)));
@@ -159,8 +159,8 @@ int diffattn_v2_cache_trim(int32_t* block_table, const int32_t* seqlens, int32_t
 int diffattn_v2_cache_free(int32_t* block_table, int32_t* seqlens, int32_t* refs, const int32_t* seqs, int32_t* result,
                            int n, int B, int max_pages, int num_pages, da2_stream_t stream) {
   if (n < 0 || !pool_ok(B, max_pages, 0, num_pages)) return DA2_ERR_INVALID;
-  if (n == 0 || B == 0) return DA2_OK;
-  if (!ints_ok(block_table, seqlens, refs, seqs, result)) return DA2_ERR_INVALID;
+  if (n == 0) return DA2_OK;
+  if (!ints_ok(refs, seqs, result) || (B > 0 && !ints_ok(block_table, seqlens))) return DA2_ERR_INVALID;
   return status_of(da2::launch_cache_free(block_table, seqlens, refs, seqs, result, n, B, max_pages, num_pages,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
