@@ -140,10 +140,23 @@ def _no_native(*_):
 _invoke = _native.invoke if _native else _no_native
 
 
+def _check_description(name, description):
+    """The native half passes every C argument as a word, whatever the prototype says: the description has
+    to name as many as the prototype has, pointers where it has pointers."""
+    arguments, words = description.split("=>")[0].split("->")
+    tensors = {a.lstrip(">@").split(":")[0].split("(")[0] for a in arguments.split() if ":" in a or a[0] == "@"}
+    got = ["pointer" if w in tensors or w == "%" else "integer" for w in words.split()] + ["pointer"]  # the stream
+    want = ["pointer" if t in (_vp, _ip) else "integer" for t in _SIGNATURES[name][1]]
+    sizes = [a.count(",") + 1 for a in arguments.split() if a[0] == "@"]
+    if got != want or any(n != len(_SIGNATURES[name + "_workspace_size"][1]) for n in sizes):
+        raise TypeError(f"{name}: the description passes {got}, the prototype takes {want}")
+
+
 def _entry(name, description):
     """An entry point of short calls: the native half checks its tensors, allocates the outputs that
     are not given and calls it on their device and the given or current stream, as described (see
     csrc/binding.cpp for the notation)."""
+    _check_description(name, description)
     return _native.define(name, description) if _native else None
 
 

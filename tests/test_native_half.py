@@ -86,3 +86,26 @@ def test_the_other_entry_points_load_without_it(tmp_path, case):
     assert out.returncode == 0, out.stderr
     lines = out.stdout.splitlines()
     assert len(lines) == 3 and all("differential_attention_v2_b200.build" in x for x in lines), out.stdout
+
+
+ROPE = """q:io<T,Hq,D> k:io<T,Hkv,D>? positions:i32[%.n,T] inv_freq:f32[%.sum] %sections
+    >q_out:io<T,Hq,D> >k_out:io<T,Hkv,D>?k !inverse !interleaved
+    -> q k q_out k_out positions inv_freq % %.n T Hq Hkv D q.s k.s q_out.s k_out.s io interleaved inverse => q_out"""
+SIZED = """q:bf16[B,S,Hq,D] k:bf16[B,S,Hkv,D] v:bf16[B,S,Hkv,D] lam:f32[B,S,Hq/2] o_branch:f32[B,S,Hq,D]
+    lse:f32[B,S,Hq] dout:bf16[B,S,Hq/2,D] #window #sink >dq:bf16[B,S,Hq,D] >dk:bf16[B,S,Hkv,D] >dv:bf16[B,S,Hkv,D]
+    >dlam:f32[B,S,Hq/2] @workspace(B,S,Hq,Hkv,window,sink)
+    -> q k v lam o_branch lse dout dq dk dv dlam B S Hq Hkv D window sink workspace workspace.n => dq"""
+
+
+def test_a_description_that_does_not_fit_its_prototype_is_refused():
+    from differential_attention_v2_b200 import _lib
+
+    _lib._check_description("diffattn_v2_rope", ROPE)
+    _lib._check_description("diffattn_v2_backward_window_sink", SIZED)
+    for name, right, a, b in (("rope", ROPE, " k.s", ""), ("rope", ROPE, " inverse =>", " inverse D =>"),
+                              ("rope", ROPE, "T Hq Hkv D q.s", "q Hq Hkv D q.s"), ("rope", ROPE, "% %.n", "%.n %"),
+                              ("backward_window_sink", SIZED, "(B,S,", "(S,"),
+                              ("backward_window_sink", SIZED, "workspace workspace.n", "workspace")):
+        assert a in right
+        with pytest.raises(TypeError):
+            _lib._check_description("diffattn_v2_" + name, right.replace(a, b))
