@@ -458,7 +458,11 @@ PyObject* invoke(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
   for (size_t i = 0; i < e.items.size(); ++i) {
     const Item& it = e.items[i];
     if (it.kind != Kind::kOut) continue;
-    if (it.only_with >= 0 && a[it.only_with] == Py_None) continue;
+    if (it.only_with >= 0 && a[it.only_with] == Py_None) {
+      if (a[i] == Py_None) continue;
+      PyErr_Format(PyExc_ValueError, "%s: there is no %s", it.name.c_str(), e.items[it.only_with].name.c_str());
+      return nullptr;
+    }
     if (a[i] != Py_None) {
       if (!c.take(it, a[i])) return nullptr;
       continue;
