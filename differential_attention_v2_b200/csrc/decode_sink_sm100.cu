@@ -29,6 +29,8 @@
 //    row, a page that now belongs to another sequence): their scores are replaced, not scaled,
 //    and their V rows are zeroed in shared memory, so no NaN or infinity passes through 0 * V.
 
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "bounds.cuh"
@@ -408,17 +410,49 @@ decode_sink_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
 }
 
 // CTAs per (KV head, sequence): as many as fit the GPU at two CTAs per SM, but no more than there are
-// groups of 64 keys; 16 (a non-portable size whose receive buffers leave one CTA per SM) only for long
-// lists and few clusters. Measured on B200 (us, 8 KV heads, 4 sinks; CTAs per cluster 1 / 2 / 4 / 8 / 16):
-//   B=1,  window 1024    15.0  10.9   9.3   7.8   9.0
-//   B=1,  window 32768    307   157    83    45    31
-//   B=8,  window 4096    44.4  27.9  28.0  32.7  55.1
-//   B=32, window 1024    27.4  32.4  45.1  67.7   155
-// (before the partials were stored ahead of the barrier, which took about 1 us off each).
-int cluster_size(long long units, int span) {
+// groups of 64 keys. 16 (a non-portable size whose receive buffers leave one CTA per SM) only where all
+// clusters of it are resident together: it needs 16 SMs of one GPC, which 7 clusters at a time found on
+// the B200 measured here. us in a graph, 4 sinks, groups of 8; CTAs per cluster 1 / 2 / 4 / 8 / 16:
+//   units (KV heads x sequences)  window
+//   1      1024    14.6  10.0   7.6   6.5   6.2      7      1024       .     .   7.7   6.6   6.3
+//   1      8192    79.4  42.1  23.3  14.3  10.0      7      8192       .     .  23.6  14.5  10.4
+//   1     32768     300   153    79  42.4  24.1      7     32768       .     .    82  43.6  25.9
+//   8      1024    14.7  10.0   7.8   6.5  10.6      8     32768     306   156    81  43.7  48.5
+//   32     1024    15.0  10.1   8.1   7.9  27.8      64     4096    44.2  27.1  26.6  31.3  69.7
+//   128    1024    16.9  16.2  21.6  29.7  99.2      256    1024    27.3  31.4  39.7  56.3   200
+int cluster_size(long long units, int span, int resident16) {
   int c = 1;
-  while (c < kMaxCluster && 2 * c * units <= (c < 8 ? 296 : 148) && span > c && (c < 8 || span >= 256)) c *= 2;
-  return c;
+  while (c < 8 && 2 * c * units <= 296 && span > c) c *= 2;
+  return c == 8 && span > 8 && units <= resident16 ? 16 : c;
+}
+
+// How many clusters of 16 the current device runs at a time (GPUs differ in the SMs of their GPCs);
+// asked once per device and kernel.
+template <int NT>
+cudaError_t resident_clusters_of_16(int* n) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];  // 1 + the number, 0: not asked yet
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < kDevices && known[device] > 0) {
+    *n = known[device] - 1;
+    return cudaSuccess;
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kMaxCluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmemBytes;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, decode_sink_kernel<NT>, &cfg);
+  if (e != cudaSuccess) return e;
+  if (device < kDevices) known[device] = 1 + *n;
+  return cudaSuccess;
 }
 
 }  // namespace decode_sink
@@ -446,15 +480,20 @@ cudaError_t launch_decode_sink(const CUtensorMap& tmK, const CUtensorMap& tmV, c
   // most groups of 64 keys that a sequence can have
   const long long keys = static_cast<long long>(window) + sink;
   const int span = static_cast<int>((keys < Smax ? keys : Smax) / 64) + 1;
-  const int c = cluster_size(static_cast<long long>(B) * Hkv, span);
-  auto kernel = Hq / Hkv > 8 ? decode_sink_kernel<2> : decode_sink_kernel<1>;
-  const uint32_t smem = smem_bytes(Hq / Hkv / 2, c);
+  const bool wide = Hq / Hkv > 8;
+  auto kernel = wide ? decode_sink_kernel<2> : decode_sink_kernel<1>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
   if (e != cudaSuccess) return e;
-  if (c > 8) {
+  const long long units = static_cast<long long>(B) * Hkv;
+  int resident16 = 0;
+  if (units * 16 <= 148) {  // (else none of it is asked for)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    e = wide ? resident_clusters_of_16<2>(&resident16) : resident_clusters_of_16<1>(&resident16);
+    if (e != cudaSuccess) return e;
   }
+  const int c = cluster_size(units, span, resident16);
+  const uint32_t smem = smem_bytes(Hq / Hkv / 2, c);
   return launch_chained(kernel, dim3(static_cast<unsigned>(c), static_cast<unsigned>(Hkv), static_cast<unsigned>(B)),
                         dim3(kThreads), smem, c, stream, tmK, tmV, p);
 }

@@ -157,3 +157,18 @@ def test_largest_masks_are_the_causal_one(da):
         _grads_close(got, ora.prefill_backward(inp["q"], inp["k"], inp["v"], inp["lam"], inp["dout"]), f"{w} {s}")
         bf16_close(da.decode(*step, window=w, sink=s), ora.prefill(inp["q"], inp["k"], inp["v"], inp["lam"])[:, -1], "decode")
     _ok(da)
+
+
+@pytest.mark.parametrize("Hq,Hkv,B", [(8, 1, 1), (16, 1, 7), (8, 4, 2), (32, 8, 1)])
+@pytest.mark.parametrize("window,sink", [(500, 4), (513, 0), (600, 100), (2100, 17)])
+def test_decode_of_few_units_by_large_clusters(da, Hq, Hkv, B, window, sink):
+    """One to nine (KV head, sequence) units: clusters of 16 CTAs or 8, with lists from two chunks a CTA on,
+    one CTA of a shorter sequence left without any."""
+    lens = [2500, 700, 1, 520, 0, 2499, 33][:B]
+    inp = _decode_inputs(Hq, Hkv, lens, seed=window + B)
+    ref = ora.decode(inp["q"], inp["kcache"], inp["vcache"], inp["seqlens"], inp["lam"], window=window, sink=sink)
+    _hide(inp, window, sink)
+    d = {k: v.cuda() for k, v in inp.items() if isinstance(v, torch.Tensor)}
+    out = da.decode(d["q"], d["kcache"], d["vcache"], d["seqlens"], d["lam"], window=window, sink=sink)
+    _ok(da)
+    bf16_close(out, ref, "few units")
