@@ -283,3 +283,37 @@ def test_the_first_call_of_a_host_thread(da, x, name):
     torch.cuda.synchronize()
     assert not isinstance(got[0], Exception), got[0]
     assert all(torch.equal(a, b) for a, b in zip(got[0], ref))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("calls", [SINK_ROPE_CACHE, PLAIN], ids=["sink", "plain"])
+def test_a_captured_call_on_a_forked_stream(da, x, calls, raw):
+    """stream= names a stream that joined the capture: outputs and workspaces come from the graph's pool, and
+    a replay after other work has used the memory gives the same bits."""
+    s = torch.cuda.Stream()
+    given = s.cuda_stream if raw else s
+    names = ["prefill_train", "backward", "backward_varlen", "decode", "decode_paged"]
+    made = [calls[n](da, x, given) for n in names]
+    refs = []
+    for call in made:
+        out = _tensors(call())
+        torch.cuda.synchronize()
+        refs.append([t.clone() for t in out])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        outs = [_tensors(call()) for call in made]
+        torch.cuda.current_stream().wait_stream(s)
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    for o in outs:
+        for t in o:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    del junk
+    for o, r, n in zip(outs, refs, names):
+        assert all(torch.equal(a, b) for a, b in zip(o, r)), n
+    assert da.device_error() == 0
