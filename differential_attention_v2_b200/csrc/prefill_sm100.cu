@@ -477,8 +477,9 @@ __device__ __forceinline__ void arrive_for_mma(uint32_t bar, int lane) {
 // kSink (with kWindow, one CTA per item): the first p.sink keys stay visible below the window. The sink
 // tiles come first, so that a row's running max starts at its sinks', then the window's. Bound as the
 // window form by each branch's chain of softmax and MMAs, and by its half-masked tiles: 2 x 4096 tokens,
-// 64/8 heads, window 1024, 4 sinks 295 us (819 TFLOP/s counted; ten 128-key tiles run for eight tiles'
-// worth of visible keys). A narrow form of a tile with few sinks (32 columns of softmax, two K-steps of
+// 64/8 heads, window 1024, 4 sinks 294 us in a graph (821 TFLOP/s counted; ten 128-key tiles run for eight
+// tiles' worth of visible keys), 322 to 327 for one call after the other, where the power cap slows it. A
+// narrow form of a tile with few sinks (32 columns of softmax, two K-steps of
 // P V) measured 299 and is not built.
 // kFine (with kSink, training): P of the tiles that hold sinks enters P V as two bf16 terms, over S's
 // other 64 columns. The sinks' weights are most of a row's, and O_b's error through their rounding is

@@ -581,7 +581,8 @@ DA2_API int diffattn_v2_rope_append_paged(const void* q, const void* k, const vo
  * At most 2^30 pages, and 2^30 tokens in a row of the table.
  * One table serves every layer with the same window and sinks. Free pages are taken lowest index
  * first, so the result of a call is unique. result int32 [1] (device) tells what happened; a call
- * that refuses changes nothing else but `copies`, which it fills with -1.
+ * that refuses changes nothing else but `copies`, which it fills with -1. A call on nothing (n == 0;
+ * for extend and trim B == 0) launches nothing and leaves result as it is.
  *
  * extend: n_new[b] (negative: 0) more tokens for every sequence: seqlens grows, and logical pages
  *   that did not exist get a page, in the order of (b, logical page). result: pages taken, or -1:

@@ -172,3 +172,27 @@ def test_decode_of_few_units_by_large_clusters(da, Hq, Hkv, B, window, sink):
     out = da.decode(d["q"], d["kcache"], d["vcache"], d["seqlens"], d["lam"], window=window, sink=sink)
     _ok(da)
     bf16_close(out, ref, "few units")
+
+
+@pytest.mark.parametrize("page", [1024, 4096])
+def test_large_pages(da, page):
+    """Appended to and decoded from; a page holds the sinks, the window and rows that nobody wrote."""
+    Hq, Hkv, n, window, sink = 16, 2, 5000, 700, 9
+    g = torch.Generator(device="cuda").manual_seed(page)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, lam = r(n, Hq, 128), r(n, Hkv, 128), r(n, Hkv, 128), torch.rand(1, Hq // 2, generator=g, device="cuda")
+    N = -(-n // page) + 2
+    kc = torch.full((N, page, Hkv, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    ints = dict(dtype=torch.int32, device="cuda")
+    table, lens, refs = torch.full((1, N - 1), -1, **ints), torch.zeros(1, **ints), torch.zeros(N, **ints)
+    refs[0] = 1  # taken by another table
+    assert da.cache_extend(table, lens, refs, torch.full((1,), n, **ints), page).item() == N - 2
+    pos = torch.arange(n, **ints)[None]
+    inv = 10000.0 ** (-torch.arange(64, device="cuda") / 64)
+    qr = da.rope_append_paged(q, k, v, pos, inv, (64,), kc, vc, table, lens, cu_seqlens=torch.tensor([0, n], **ints))
+    kr = da.rope(k, None, pos, inv, (64,))[0]
+    out = da.decode_paged(qr[-1:].clone(), kc, vc, table, lens, lam, window=window, sink=sink)
+    _ok(da)
+    ref = ora.decode(qr[-1:].cpu(), kr[None].cpu(), v[None].cpu(), [n], lam.cpu(), window=window, sink=sink)
+    bf16_close(out, ref, "large pages")
