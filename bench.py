@@ -73,8 +73,8 @@ SPEC_HBM_GBS = 8000.0
 # one launch), keyed by workload and by the kernel source it was taken on; reported as null
 # once the source differs from the one captured.
 NCU_TRAFFIC = {
-    # B=1 x 32768 causal prefill: 3713148672 read + 248252160 written
-    ("prefill", "prefill_b1_s32768"): {"bytes": 3961400832, "source_sha": "14ed30a2132bf5d8"},
+    # B=1 x 32768 causal prefill: 3460585216 read + 247282944 written
+    ("prefill", "prefill_b1_s32768"): {"bytes": 3707868160, "source_sha": "fb98ff21766a0026"},
     # B=8 x 131072 needle decode (split kernel with the fused merge): 4304143616 + 12096256
     ("decode", "needle_decode_b8_s131072"): {"bytes": 4316239872, "source_sha": "ad1318f4ff5b5a63"},
 }
