@@ -449,8 +449,10 @@ cudaError_t resident_clusters_of_16(int* n) {
   cfg.dynamicSmemBytes = kMaxSmemBytes;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(n, decode_sink_kernel<NT>, &cfg);
-  if (e != cudaSuccess) return e;
+  if (cudaOccupancyMaxActiveClusters(n, decode_sink_kernel<NT>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    *n = 0;  // a device without such clusters: 8 CTAs do
+  }
   if (device < kDevices) known[device] = 1 + *n;
   return cudaSuccess;
 }
@@ -486,7 +488,7 @@ cudaError_t launch_decode_sink(const CUtensorMap& tmK, const CUtensorMap& tmV, c
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(B) * Hkv;
   int resident16 = 0;
-  if (units * 16 <= 148) {  // (else none of it is asked for)
+  if (units <= 148 / kMaxCluster) {  // (more cannot be resident at one CTA per SM)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     e = wide ? resident_clusters_of_16<2>(&resident16) : resident_clusters_of_16<1>(&resident16);

@@ -24,8 +24,9 @@ inline int page_shift_of(int page_size) {
 // Launches a kernel that begins with pdl_wait(), so that the launch overlaps the end of the kernel
 // before it in the stream; cluster > 0 gives the cluster's size. Passes called one after the other, us,
 // with and without: one user's decode 6.0 and 8.2, five page operations 22.8 and 32.8, rotary append of
-// 64 tokens 5.1 and 6.2, packed training step 114 and 125. (Letting the next kernel in as soon as this one's CTAs run fills the SMs with
-// waiting CTAs: rotary of 2,049 tokens 9.8 and 7.5 us with that before and after the wait, 5.0 without.)
+// 64 tokens 5.1 and 6.2, packed training step 114 and 125. (Letting the next kernel in as soon as this
+// one's CTAs run fills the SMs with waiting CTAs: rotary of 2,049 tokens 9.8 and 7.5 us with that before
+// and after the wait, 5.0 without.)
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream,
                            const A&... args) {
